@@ -51,7 +51,9 @@ typedef enum {
     LF_ERR_UNSUPPORTED_DEVICE = 11,  /* current device is not compute capability 10.0 */
     LF_ERR_WORKSPACE = 12,           /* workspace pointer/size too small */
     LF_ERR_TOO_LARGE = 13,           /* a size exceeds the documented maximum */
-    LF_ERR_SCRATCH_LIMIT = 14        /* shape needs more scratch than lf_attention_forward_noalloc holds */
+    LF_ERR_SCRATCH_LIMIT = 14,       /* shape needs more scratch than lf_attention_forward_noalloc holds */
+    LF_ERR_BAD_LENGTHS = 15,         /* sequence offsets or lengths that do not fit (device status word) */
+    LF_ERR_BAD_PAGE = 16             /* a needed page is missing from the page table (device status word) */
 } lf_status;
 
 typedef enum { LF_F32 = 0, LF_F16 = 1, LF_BF16 = 2 } lf_dtype;
@@ -67,7 +69,7 @@ int lf_version(void);
  * content-dependent error recorded by this library's kernels on the current
  * device since the last reset (LF_OK if none).  reset != 0 clears the word.
  * Errors recorded: LF_ERR_G_GT_W, LF_ERR_GLOBAL_NOT_PREFIX,
- * LF_ERR_DEVICE_TIMEOUT.
+ * LF_ERR_DEVICE_TIMEOUT, LF_ERR_BAD_LENGTHS, LF_ERR_BAD_PAGE.
  */
 lf_status lf_device_status(lf_stream_t stream, int reset);
 
@@ -406,6 +408,193 @@ lf_status lf_noalloc_device_status(lf_stream_t stream, int reset);
  * `stream`; nothing else is in flight in that CTA when the wait gives up.
  */
 lf_status lf_selftest_bounded_wait(unsigned long long limit_ns, lf_stream_t stream);
+
+/*
+ * Windowed causal attention with sinks (decoder form of the sliding window;
+ * no counterpart on the pages).  In a sequence of n tokens, with s = scale
+ * and kv(h) = h / (Hq / Hkv) the key/value head of query head h, the query at
+ * position i sees the keys
+ *     K_i = { j <= i : i - j <= w  or  j < sinks },
+ *     out_i = sum_{j in K_i} softmax_j(s * q_i.k_j) v_j,
+ *     lse_i = ln sum_{j in K_i} exp(s * q_i.k_j).
+ * w >= n - 1 is plain causal attention.
+ *
+ * lf_heads: a view of per-head rows of 64 elements; the row of (batch b,
+ * head h, token t) starts at data + b * batch_stride + h * head_stride +
+ * t * token_stride (strides in elements).  The 64 elements are contiguous;
+ * data and all strides are multiples of 16 bytes; the strides are positive
+ * and rows of an output view must not overlap.  The stride of a dimension
+ * of size 1 is not used.  So [B, H, L, 64], [T, H, 64] and slices of a fused
+ * projection's output all fit.
+ */
+typedef struct {
+    void* data;
+    long long batch_stride, head_stride, token_stride;
+} lf_heads;
+
+/*
+ * lf_window_attention_forward -- the attention above.
+ *   Packed sequences (cu_seqlens != NULL): the views hold L tokens in all
+ *     and one batch; sequence b is tokens cu_seqlens[b] .. cu_seqlens[b+1]-1
+ *     ([n_seqs + 1] int32, device, ascending; sequences may be empty).  Rows
+ *     of tokens in no sequence are left as they were in every output.
+ *     seq_lens must be NULL.
+ *   Padded sequences (cu_seqlens == NULL): batch b of the views holds L rows,
+ *     the first seq_lens[b] ([n_seqs] int32, device; NULL: all L) its tokens.
+ *     Rows past them are written as zeros (lse: -infinity).
+ *   q          view with Hq heads; k, v views with Hkv heads, Hq a multiple
+ *              of Hkv, Hq / Hkv <= 64
+ *   w, sinks   >= 0;  scale > 0 and finite
+ *   out        [B, L, Hq * 64] of dtype, dense (B = 1 when packed)
+ *   lse        [B, Hq, L] float32, dense; for the backward pass
+ * dtype: LF_F32 (CUDA cores), LF_F16, LF_BF16 (tensor cores, fp32
+ * accumulation and softmax).  Values outside every K_i (padding, other
+ * sequences' rows) may be anything, NaN included; a NaN or infinity inside a
+ * sequence may reach any row of that sequence.
+ * Errors: LF_ERR_NULL, LF_ERR_BAD_DIM (sizes, heads, scale, strides <= 0,
+ * both cu_seqlens and seq_lens), LF_ERR_DTYPE, LF_ERR_MISALIGNED (also a
+ * stride that is not a multiple of 16 bytes), LF_ERR_TOO_LARGE
+ * (n_seqs * Hq * L or n_seqs * sinks >= 2^31, L >= 2^30, n_seqs >= 2^23,
+ * Hkv > 65535).
+ * Offsets or lengths outside [0, L] or descending are clamped and recorded
+ * as LF_ERR_BAD_LENGTHS.  L = 0 is allowed and does nothing.  Asynchronous;
+ * no scratch, so calls on different streams may overlap.
+ */
+lf_status lf_window_attention_forward(const lf_heads* q, const lf_heads* k, const lf_heads* v,
+                                      const int32_t* cu_seqlens, const int32_t* seq_lens, int n_seqs, int Hq,
+                                      int Hkv, int L, int w, int sinks, float scale, lf_dtype dtype,
+                                      lf_stream_t stream, void* out, float* lse);
+
+/* Bytes of workspace lf_window_attention_backward needs (0 on bad sizes). */
+size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int Hq, int Hkv, int L, int w, int sinks);
+
+/*
+ * lf_window_attention_backward -- gradients of lf_window_attention_forward.
+ * With P the softmax (recomputed from lse), dP_ij = dout_i.v_j and
+ * delta_i = dout_i.out_i:
+ *     dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dP_ij - delta_i),
+ *     dq_i = s sum_j dS_ij k_j,   dk_j = s sum_i dS_ij q_i,
+ * summed over the Hq / Hkv query heads of a key/value head.  P and dS are
+ * rounded to dtype as tensor-core operands (LF_F32: not rounded); every sum
+ * is fp32 and has a fixed order, so results repeat bit for bit.
+ *   out, lse   as the forward call wrote them;  dout [B, L, Hq * 64], dense
+ *   dq, dk, dv views like q, k, v, written in full (rows past a sequence's
+ *              tokens as the forward call's out: left, or zeros)
+ *   workspace  device memory of at least
+ *              lf_window_attention_backward_workspace_bytes(...) bytes,
+ *              256-byte aligned, contents arbitrary.  Calls (or captured
+ *              graphs) that may overlap need workspaces of their own.
+ * Errors as the forward call's, and LF_ERR_WORKSPACE.  Asynchronous.
+ */
+lf_status lf_window_attention_backward(const lf_heads* q, const lf_heads* k, const lf_heads* v, const void* out,
+                                       const float* lse, const void* dout, const int32_t* cu_seqlens,
+                                       const int32_t* seq_lens, int n_seqs, int Hq, int Hkv, int L, int w, int sinks,
+                                       float scale, lf_dtype dtype, void* workspace, size_t workspace_bytes,
+                                       lf_stream_t stream, const lf_heads* dq, const lf_heads* dk,
+                                       const lf_heads* dv);
+
+/*
+ * A paged key/value cache: num_pages pages of page_size positions (a power
+ * of two from 8 to 4096) for Hkv heads, k_cache and v_cache views with the
+ * page as the batch and the position in the page as the token (for example
+ * [num_pages, Hkv, page_size, 64], or [num_pages, page_size, Hkv, 64] with
+ * its strides).  block_table [n_seqs, max_pages] int32, device: entry k of
+ * sequence b is the page of its positions k * page_size ...; entries of
+ * pages that no call needs any more (wholly behind the window, and holding
+ * no sink) may be anything, for example -1 once freed.
+ *
+ * One call works on T new tokens, packed: sequence b's are rows cu_seqlens[b]
+ * .. cu_seqlens[b+1]-1 (possibly none), and stand at its last positions:
+ * kv_lens[b] ([n_seqs] int32, device) counts the sequence's positions with
+ * the new ones.
+ *
+ * lf_paged_cache_append -- copies the new tokens' k_new, v_new (views, one
+ * batch of T tokens, Hkv heads; LF_F16 or LF_BF16) into the cache.  A token
+ * whose page is missing (a table entry outside [0, num_pages), a position
+ * past the table's width) is not written and recorded as LF_ERR_BAD_PAGE; a
+ * position below 0 (kv_lens[b] smaller than its number of new tokens) as
+ * LF_ERR_BAD_LENGTHS.
+ */
+lf_status lf_paged_cache_append(const lf_heads* k_new, const lf_heads* v_new, const lf_heads* k_cache,
+                                const lf_heads* v_cache, const int32_t* block_table, const int32_t* cu_seqlens,
+                                const int32_t* kv_lens, int n_seqs, int Hkv, int T, int max_pages, int num_pages,
+                                int page_size, lf_dtype dtype, lf_stream_t stream);
+
+/* Bytes of workspace lf_paged_attention_forward needs (0 if none, or on bad
+ * sizes). */
+size_t lf_paged_attention_workspace_bytes(int n_seqs, int Hq, int Hkv, int T, int max_q_len, int max_pages,
+                                          int page_size, int w, int sinks);
+
+/*
+ * lf_paged_attention_forward -- windowed causal attention with sinks (as
+ * above) of the T new tokens over the cache, which already holds their own
+ * keys and values.  The token t of sequence b stands at position
+ * kv_lens[b] - n_b + t.
+ *   q           view, one batch of T tokens, Hq heads
+ *   max_q_len   no sequence has more new tokens (host bound; a longer one is
+ *               recorded as LF_ERR_BAD_LENGTHS and its rows are left as they
+ *               were)
+ *   out         [T, Hq * 64] of dtype, dense; rows in no sequence are left
+ *   workspace   as lf_paged_attention_workspace_bytes, 256-byte aligned,
+ *               contents arbitrary (NULL when that is 0); partial results of
+ *               long contexts split over several CTAs.  Calls (or captured
+ *               graphs) that may overlap need workspaces of their own.
+ * dtype LF_F16 or LF_BF16.  Keys and values of positions no query sees, and
+ * of slots past kv_lens[b], may be anything, NaN included.  A needed page
+ * that is missing is recorded as LF_ERR_BAD_PAGE and its keys are left out;
+ * a token with no key left, or at a position below 0 (recorded as
+ * LF_ERR_BAD_LENGTHS), gets zeros.  kv_lens[b] beyond the table's width is
+ * clamped and recorded as LF_ERR_BAD_LENGTHS.
+ * Errors: LF_ERR_NULL, LF_ERR_BAD_DIM, LF_ERR_DTYPE, LF_ERR_MISALIGNED,
+ * LF_ERR_TOO_LARGE (T * Hq >= 2^31, max_pages * page_size >= 2^30, n_seqs >=
+ * 2^23, Hkv > 65535), LF_ERR_WORKSPACE.  T = 0 does nothing.  Asynchronous.
+ */
+lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache, const lf_heads* v_cache,
+                                     const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* kv_lens,
+                                     int n_seqs, int Hq, int Hkv, int T, int max_q_len, int max_pages, int num_pages,
+                                     int page_size, int w, int sinks, float scale, lf_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, lf_stream_t stream, void* out);
+
+/*
+ * lf_layer_norm_forward -- layer norm of each row (the LayerNorm of FTL
+ * §Longformer Encoder 计算流程 / 每个 Transformer 层 steps 5 and 6 without its
+ * bias and residual), statistics kept for the gradient:
+ *     y = (x - mean) * rstd * gamma + beta,  rstd = 1 / sqrt(var + eps)
+ * with the population variance.
+ *   x      rows of N elements of dtype (LF_F32, LF_F16, LF_BF16), x_stride
+ *          elements apart (>= N)
+ *   gamma, beta  [N] float32, or NULL (1, 0)
+ *   y      [rows, N] of dtype, dense
+ *   mean, rstd   [rows] float32, or NULL when no gradient is wanted
+ * 1 <= N <= 16384 (LF_ERR_TOO_LARGE above), eps >= 0 and finite; rows = 0
+ * does nothing.  Errors: LF_ERR_NULL, LF_ERR_BAD_DIM, LF_ERR_DTYPE,
+ * LF_ERR_MISALIGNED (pointers; strides are free).  Asynchronous, no scratch.
+ */
+lf_status lf_layer_norm_forward(const void* x, long long x_stride, const float* gamma, const float* beta, int rows,
+                                int N, float eps, lf_dtype dtype, lf_stream_t stream, void* y, float* mean,
+                                float* rstd);
+
+/* Bytes of workspace lf_layer_norm_backward needs for dgamma / dbeta (0 on
+ * bad sizes). */
+size_t lf_layer_norm_backward_workspace_bytes(int rows, int N);
+
+/*
+ * lf_layer_norm_backward -- gradients of lf_layer_norm_forward: with
+ * xh = (x - mean) rstd and g = dy gamma,
+ *     dx = rstd (g - mean(g) - xh mean(g xh)),
+ *     dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy.
+ *   dy     rows of N elements of dtype, dy_stride apart
+ *   mean, rstd   as the forward call wrote them
+ *   dx     [rows, N] of dtype, dense
+ *   dgamma, dbeta  [N] float32, each may be NULL; written (not added to);
+ *          zeros for rows = 0.  The sums have a fixed order.
+ *   workspace  as above, 256-byte aligned, contents arbitrary; not needed
+ *          when dgamma and dbeta are both NULL
+ */
+lf_status lf_layer_norm_backward(const void* dy, long long dy_stride, const void* x, long long x_stride,
+                                 const float* gamma, const float* mean, const float* rstd, int rows, int N,
+                                 lf_dtype dtype, void* workspace, size_t workspace_bytes, lf_stream_t stream,
+                                 void* dx, float* dgamma, float* dbeta);
 
 #ifdef __cplusplus
 }

@@ -168,6 +168,8 @@ const char* lf_status_string(int s) {
         case LF_ERR_WORKSPACE: return "LF_ERR_WORKSPACE: workspace missing or too small";
         case LF_ERR_TOO_LARGE: return "LF_ERR_TOO_LARGE: size beyond the supported maximum";
         case LF_ERR_SCRATCH_LIMIT: return "LF_ERR_SCRATCH_LIMIT: shape needs more than the 32 MiB scratch of the no-allocation entry point";
+        case LF_ERR_BAD_LENGTHS: return "LF_ERR_BAD_LENGTHS: sequence offsets or lengths do not fit";
+        case LF_ERR_BAD_PAGE: return "LF_ERR_BAD_PAGE: a needed page is missing from the page table";
         default: return "unknown lf_status";
     }
 }

@@ -1,0 +1,110 @@
+// Internal declarations of the windowed causal attention (training and paged
+// serving) and the stand-alone layer norm.
+#pragma once
+
+#include "lf_internal.h"
+#include "lf_visible.h"
+
+namespace lf {
+
+// One call, as the kernels see it.  Sequences are packed (cu != NULL: T = L
+// rows in all) or padded (n_seqs x L rows, lens tokens).  w and sinks have
+// been clamped to the longest possible sequence; sinks is 0 when every
+// window reaches the sequence's start.
+struct WindowArgs {
+    lf_heads q, k, v;
+    const int32_t* cu;
+    const int32_t* lens;
+    int n_seqs, Hq, Hkv, L, w, sinks;
+    float scale;
+    lf_dtype dtype;
+    void* out;          // [B][L][Hq * 64]
+    float* lse;         // [B][Hq][L]
+    int* status;
+    // backward
+    const void* dout;   // [B][L][Hq * 64]
+    lf_heads dq, dk, dv;
+    float* delta;       // [B][Hq][L] workspace
+    float* part;        // partial gradients of the sink keys, see below
+    int chunk;          // tokens of one sink chunk
+    int heads_group() const { return Hq / Hkv; }
+    bool packed() const { return cu != nullptr; }
+};
+
+// Gradients of the sink keys: the queries that see a sink from outside its
+// window are cut into chunks of `chunk` tokens; chunk slot c (numbered as
+// token_tile numbers tiles) leaves its sum in
+//     part[n_seqs + c][kv head][key < sinks][dk, dv][64]
+// and the window's own contribution goes to part[sequence].  A last kernel
+// adds them in a fixed order and rounds once.
+LF_HD int sink_chunk(int w) { return w + 128 > 512 ? (w + 128 + 127) / 128 * 128 : 512; }
+LF_HD size_t sink_part_floats(int Hkv, int sinks) { return (size_t)Hkv * sinks * 2 * 64; }
+inline size_t sink_slots(const WindowArgs& a) {
+    return (size_t)a.n_seqs + token_slots(a.packed(), a.n_seqs, a.L, a.chunk);
+}
+
+lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream);
+lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream);
+lf_status launch_sink_reduce(const WindowArgs& a, cudaStream_t stream);
+
+// ---- paged cache ----
+struct PagedArgs {
+    lf_heads q;               // [T] packed new tokens
+    lf_heads k_new, v_new;    // append only
+    lf_heads k, v;            // cache: batch = page, token = slot in the page
+    const int32_t* cu;        // [n_seqs + 1]
+    const int32_t* kv_lens;   // [n_seqs]
+    const int32_t* table;     // [n_seqs][max_pages]
+    int n_seqs, Hq, Hkv, T, max_q, max_pages, num_pages, page_shift, w, sinks;
+    float scale;
+    lf_dtype dtype;
+    void* out;                // [T][Hq * 64]
+    int* status;
+    void* workspace;
+    int heads_group() const { return Hq / Hkv; }
+};
+// Where sequence b's n new tokens stand: kv keys in all (clamped to the
+// table's width), the first new token at position `first`.  Returns false
+// for a sequence that is not worked on (longer than max_q); `report` records
+// what does not fit.
+__device__ __forceinline__ bool paged_seq(const PagedArgs& a, int b, int n, int& kv, int& first, bool report) {
+    const int raw = a.kv_lens[b], width = a.max_pages << a.page_shift;
+    kv = iclamp(raw, 0, width);
+    first = kv - n;
+    if (report && (raw != kv || first < 0 || n > a.max_q)) record_status(a.status, b, LF_ERR_BAD_LENGTHS);
+    return n <= a.max_q;
+}
+
+// The offsets must ascend from 0 to at most L, and lengths fit; records the
+// sequences whose do not (every access is clamped anyway).  One block calls.
+__device__ __forceinline__ void check_lengths(const int32_t* cu, const int32_t* lens, int n_seqs, int L, int* status) {
+    for (int b = threadIdx.x; b < n_seqs; b += blockDim.x) {
+        const bool bad = cu ? (cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > L) : (lens && (lens[b] < 0 || lens[b] > L));
+        if (bad) record_status(status, b, LF_ERR_BAD_LENGTHS);
+    }
+}
+lf_status launch_paged_append(const PagedArgs& a, cudaStream_t stream);
+lf_status launch_paged_forward_simt(const PagedArgs& a, cudaStream_t stream);
+
+// ---- layer norm ----
+struct NormArgs {
+    const void* x;
+    const void* dy;
+    long long x_stride, dy_stride;  // elements between rows
+    const float* gamma;             // [N] or NULL
+    const float* beta;              // [N] or NULL
+    int rows, N;
+    float eps;
+    lf_dtype dtype;
+    void* y;                        // forward output, backward dx: [rows][N]
+    float* mean;                    // [rows] (may be NULL in the forward pass)
+    float* rstd;
+    float* dgamma;                  // [N] or NULL
+    float* dbeta;
+    float* part;                    // workspace, NULL when neither is wanted
+};
+lf_status launch_norm_forward(const NormArgs& a, cudaStream_t stream);
+lf_status launch_norm_backward(const NormArgs& a, cudaStream_t stream);
+size_t norm_backward_bytes(int rows, int N);
+
+}  // namespace lf

@@ -1,0 +1,565 @@
+// Windowed causal attention with sinks on the CUDA cores: forward, backward
+// and the paged form, for every dtype (fp32 arithmetic throughout).
+//
+//   forward   one CTA per tile of 64 query rows (64 / G tokens times the G
+//             query heads of a key/value head), online softmax over blocks
+//             of 64 keys:  m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'),
+//             O' = O 2^(m - m') + P V.
+//   backward  dQ: one CTA per query tile;  dK, dV: one CTA per block of 64
+//             keys, over the query tiles that see it, all G heads of the
+//             group in one accumulator.  P is recomputed from the saved
+//             log-sum-exp.  Each sum has one owner and one order: no atomics.
+//
+// The three products of a block pair run from shared memory with a 4 x 4
+// register tile per thread (8 float4 loads for 64 FMAs).
+#include "lf_convert.cuh"
+#include "lf_window.h"
+
+namespace lf {
+namespace {
+
+constexpr int kT = 64;      // rows and keys per tile
+constexpr int kD = 64;      // head dim
+constexpr int kLd = 68;     // padded row of a shared tile (floats)
+constexpr int kThreads = 256;
+constexpr int kTile = kT * kLd;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load4<__half>(const __half* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = Pair<__half>::unpack(u.x), b = Pair<__half>::unpack(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = Pair<__nv_bfloat16>::unpack(u.x), b = Pair<__nv_bfloat16>::unpack(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// 64 rows of 64 into a shared tile; row(r) is the row's address, NULL: zeros.
+template <typename T, typename F>
+__device__ __forceinline__ void load_tile(float* dst, F row) {
+    const int c = (threadIdx.x & 15) * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (threadIdx.x >> 4) + 16 * i;
+        const T* p = row(r);
+        *reinterpret_cast<float4*>(dst + r * kLd + c) = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j]
+__device__ __forceinline__ void tile_nt(float (&acc)[4][4], const float* A, const float* B, int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < kD; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * kLd + d);
+            b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * kLd + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][0..3] += sum_k P[4 ty + i][k] V[k][4 tx ..]
+__device__ __forceinline__ void tile_nn(float (&acc)[4][4], const float* P, const float* V, int ty, int tx) {
+#pragma unroll 4
+    for (int k = 0; k < kT; k += 4) {
+        float4 p[4], v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[i] = *reinterpret_cast<const float4*>(P + (4 * ty + i) * kLd + k);
+            v[i] = *reinterpret_cast<const float4*>(V + (k + i) * kLd + 4 * tx);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float pk[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][0] = fmaf(pk[j], v[j].x, acc[i][0]);
+                acc[i][1] = fmaf(pk[j], v[j].y, acc[i][1]);
+                acc[i][2] = fmaf(pk[j], v[j].z, acc[i][2]);
+                acc[i][3] = fmaf(pk[j], v[j].w, acc[i][3]);
+            }
+        }
+    }
+}
+
+// Sum / max over the 16 threads that share ty.
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* view_row(const lf_heads& v, int batch, int head, int token) {
+    return static_cast<const T*>(v.data) + batch * v.batch_stride + head * v.head_stride + token * v.token_stride;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) p[c] = from_f<T>(x[c]);
+}
+template <>
+__device__ __forceinline__ void store4<float>(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ WindowArgs a) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + kTile, *V = K + kTile, *P = V + kTile;
+    const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status);
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, blockIdx.x);
+    if (t.t0 >= t.rows) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    auto q_row = [&](int r) -> const T* {
+        const int i = t.t0 + r / G;
+        return r < TQ * G && i < t.n ? view_row<T>(a.q, t.batch, hk * G + r % G, t.start + i) : nullptr;
+    };
+    load_tile<T>(Q, q_row);
+    float m[4], l[4], o[4][4];
+    int pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        pos[i] = r < TQ * G ? t.t0 + r / G : INT32_MAX;
+        if (pos[i] >= t.n) pos[i] = -1;  // sees nothing
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+    }
+    const float sc = a.scale * kLog2e;
+    const int i1 = imin(t.t0 + TQ, t.n) - 1;
+    KeyBlocks kb = {0, 0, 0};
+    if (t.t0 < t.n) kb = key_blocks(t.t0, i1, t.n, a.w, a.sinks, kT);
+    for (int n = 0; n < kb.n; ++n) {
+        const int c0 = key_block(kb, n) * kT;
+        __syncthreads();
+        load_tile<T>(K, [&](int r) -> const T* {
+            return c0 + r < t.n ? view_row<T>(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
+        });
+        load_tile<T>(V, [&](int r) -> const T* {
+            return c0 + r < t.n ? view_row<T>(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
+        });
+        __syncthreads();
+        float s[4][4];
+        tile_nt(s, Q, K, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = c0 + tx + 16 * j;
+                s[i][j] = key_visible(pos[i], key, a.w, a.sinks) && key < t.n ? s[i][j] * sc : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            const float mn = fmaxf(m[i], max16(mx));
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - base);
+                sum += p;
+                P[(4 * ty + i) * kLd + tx + 16 * j] = p;
+            }
+            m[i] = mn;
+            l[i] = l[i] * f + sum16(sum);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[i][c] *= f;
+        }
+        __syncwarp();  // a row of P is written and read by the same half warp
+        tile_nn(o, P, V, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i, tok = t.t0 + r / G, h = hk * G + r % G;
+        if (r >= TQ * G || tok >= t.rows) continue;
+        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][c] *= inv;
+        const size_t row = (size_t)t.batch * a.L + t.start + tok;
+        store4(static_cast<T*>(a.out) + (row * a.Hq + h) * kD + 4 * tx, o[i]);
+        if (tx == 0)
+            a.lse[((size_t)t.batch * a.Hq + h) * a.L + t.start + tok] =
+                l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
+    }
+}
+
+// ---------------------------------------------------------------- dQ
+// Also leaves delta = rowsum(dO * out) for the kernels of dK and dV.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ WindowArgs a) {
+    extern __shared__ float sm[];
+    float *Q = sm, *dO = Q + kTile, *K = dO + kTile, *V = K + kTile, *S = V + kTile;
+    const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status);
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, blockIdx.x);
+    if (t.t0 >= t.rows) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    auto live = [&](int r) { return r < TQ * G && t.t0 + r / G < t.n; };
+    auto o_off = [&](int r) {
+        return (((size_t)t.batch * a.L + t.start + t.t0 + r / G) * a.Hq + hk * G + r % G) * kD;
+    };
+    load_tile<T>(Q, [&](int r) -> const T* {
+        return live(r) ? view_row<T>(a.q, t.batch, hk * G + r % G, t.start + t.t0 + r / G) : nullptr;
+    });
+    load_tile<T>(dO, [&](int r) -> const T* { return live(r) ? static_cast<const T*>(a.dout) + o_off(r) : nullptr; });
+    load_tile<T>(K, [&](int r) -> const T* { return live(r) ? static_cast<const T*>(a.out) + o_off(r) : nullptr; });
+    __syncthreads();
+    float delta[4], lse[4], acc[4][4];
+    int pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i, tok = t.t0 + r / G, h = hk * G + r % G;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            s = fmaf(dO[r * kLd + 4 * tx + c], K[r * kLd + 4 * tx + c], s);
+            acc[i][c] = 0.f;
+        }
+        delta[i] = sum16(s);
+        pos[i] = live(r) ? tok : -1;
+        lse[i] = 0.f;
+        if (live(r)) {
+            const size_t at = ((size_t)t.batch * a.Hq + h) * a.L + t.start + tok;
+            lse[i] = a.lse[at] * kLog2e;
+            if (tx == 0) a.delta[at] = delta[i];
+        }
+    }
+    const float sc = a.scale * kLog2e;
+    KeyBlocks kb = {0, 0, 0};
+    if (t.t0 < t.n) kb = key_blocks(t.t0, imin(t.t0 + TQ, t.n) - 1, t.n, a.w, a.sinks, kT);
+    for (int n = 0; n < kb.n; ++n) {
+        const int c0 = key_block(kb, n) * kT;
+        __syncthreads();
+        load_tile<T>(K, [&](int r) -> const T* {
+            return c0 + r < t.n ? view_row<T>(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
+        });
+        load_tile<T>(V, [&](int r) -> const T* {
+            return c0 + r < t.n ? view_row<T>(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
+        });
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        tile_nt(s, Q, K, ty, tx);
+        tile_nt(dp, dO, V, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = c0 + tx + 16 * j;
+                const bool vis = key_visible(pos[i], key, a.w, a.sinks) && key < t.n;
+                S[(4 * ty + i) * kLd + tx + 16 * j] =
+                    vis ? exp2f(fmaf(s[i][j], sc, -lse[i])) * (dp[i][j] - delta[i]) : 0.f;
+            }
+        __syncwarp();
+        tile_nn(acc, S, K, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i, tok = t.t0 + r / G;
+        if (r >= TQ * G || tok >= t.rows) continue;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] *= a.scale;
+        store4(const_cast<T*>(view_row<T>(a.dq, t.batch, hk * G + r % G, t.start + tok)) + 4 * tx, acc[i]);
+    }
+}
+
+// ---------------------------------------------------------------- dK, dV
+// kSink false: one block of 64 keys over the queries that hold it in their
+// window.  kSink true: one block of sink keys over a chunk of the queries
+// that see it from outside their window; writes fp32 partial sums.
+template <typename T, bool kSink>
+__global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ WindowArgs a) {
+    extern __shared__ float sm[];
+    float *K = sm, *V = K + kTile, *Q = V + kTile, *dO = Q + kTile, *P = dO + kTile, *S = P + kTile;
+    __shared__ float lse_s[kT], delta_s[kT];
+    const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.chunk : kT, blockIdx.x);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (kSink ? t.t0 >= t.n : t.t0 >= t.rows) return;
+    const int c0 = kSink ? blockIdx.z * kT : t.t0;
+    const int n_keys = kSink ? imin(t.n, a.sinks) : t.n;
+    // query tokens: [q0, q1)
+    int q0, q1;
+    if (kSink) {
+        q0 = imax(t.t0, a.w + 1);
+        q1 = imin(t.t0 + a.chunk, t.n);
+    } else {
+        q0 = c0;
+        q1 = (int)min((long long)t.n, (long long)c0 + kT + a.w);
+    }
+    load_tile<T>(K, [&](int r) -> const T* {
+        return c0 + r < t.n ? view_row<T>(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
+    });
+    load_tile<T>(V, [&](int r) -> const T* {
+        return c0 + r < t.n ? view_row<T>(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
+    });
+    float dk[4][4], dv[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dk[i][c] = dv[i][c] = 0.f;
+    const float sc = a.scale * kLog2e;
+    for (int qt = q0; qt < q1; qt += TQ) {
+        auto live = [&](int r) { return r < TQ * G && qt + r / G < q1; };
+        auto o_off = [&](int r) {
+            return (((size_t)t.batch * a.L + t.start + qt + r / G) * a.Hq + hk * G + r % G) * kD;
+        };
+        __syncthreads();
+        load_tile<T>(Q, [&](int r) -> const T* {
+            return live(r) ? view_row<T>(a.q, t.batch, hk * G + r % G, t.start + qt + r / G) : nullptr;
+        });
+        load_tile<T>(dO, [&](int r) -> const T* { return live(r) ? static_cast<const T*>(a.dout) + o_off(r) : nullptr; });
+        if (threadIdx.x < kT) {
+            const int r = threadIdx.x;
+            const size_t at = ((size_t)t.batch * a.Hq + hk * G + r % G) * a.L + t.start + qt + r / G;
+            lse_s[r] = live(r) ? a.lse[at] * kLog2e : 0.f;
+            delta_s[r] = live(r) ? a.delta[at] : 0.f;
+        }
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        tile_nt(s, K, Q, ty, tx);
+        tile_nt(dp, V, dO, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = tx + 16 * j, key = c0 + 4 * ty + i, qi = qt + r / G;
+                const bool in = qi - key <= a.w;
+                const bool vis = live(r) && key < n_keys && key <= qi && in != kSink;
+                const float p = vis ? exp2f(fmaf(s[i][j], sc, -lse_s[r])) : 0.f;
+                P[(4 * ty + i) * kLd + r] = p;
+                S[(4 * ty + i) * kLd + r] = vis ? p * (dp[i][j] - delta_s[r]) : 0.f;
+            }
+        __syncwarp();
+        tile_nn(dv, P, dO, ty, tx);
+        tile_nn(dk, S, Q, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int key = c0 + 4 * ty + i;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dk[i][c] *= a.scale;
+        if (kSink || key < a.sinks) {
+            if (key >= (kSink ? a.sinks : imin(a.sinks, t.n))) {
+                if (kSink || key >= t.rows) continue;
+            } else {
+                const size_t slot = kSink ? a.n_seqs + blockIdx.x : t.b;
+                float* p = a.part + ((slot * a.Hkv + hk) * a.sinks + key) * 2 * kD + 4 * tx;
+                store4(p, dk[i]);
+                store4(p + kD, dv[i]);
+                continue;
+            }
+        }
+        if (key >= t.rows) continue;
+        store4(const_cast<T*>(view_row<T>(a.dk, t.batch, hk, t.start + key)) + 4 * tx, dk[i]);
+        store4(const_cast<T*>(view_row<T>(a.dv, t.batch, hk, t.start + key)) + 4 * tx, dv[i]);
+    }
+}
+
+// Adds the partial gradients of the sink keys: the window's, then the
+// chunks' in order.  One 128-thread block per (key, kv head, sequence).
+template <typename T>
+__global__ void __launch_bounds__(128) sink_reduce_kernel(const __grid_constant__ WindowArgs a) {
+    const int key = blockIdx.x % a.sinks, hk = blockIdx.y, b = blockIdx.x / a.sinks, e = threadIdx.x;
+    const int start = a.cu ? iclamp(a.cu[b], 0, a.L) : 0;
+    const int n = a.cu ? iclamp(a.cu[b + 1], 0, a.L) - start : (a.lens ? iclamp(a.lens[b], 0, a.L) : a.L);
+    if (key >= n) return;
+    const size_t step = sink_part_floats(a.Hkv, a.sinks);
+    const float* p = a.part + ((size_t)hk * a.sinks + key) * 2 * kD + e;
+    float s = p[b * step];
+    const int first = a.cu ? start / a.chunk + b : b * ((a.L + a.chunk - 1) / a.chunk);
+    const int chunks = (n + a.chunk - 1) / a.chunk;
+    for (int c = 0; c < chunks; ++c) s += p[(size_t)(a.n_seqs + first + c) * step];
+    const lf_heads& v = e < kD ? a.dk : a.dv;
+    const_cast<T*>(view_row<T>(v, a.cu ? 0 : b, hk, start + key))[e & (kD - 1)] = from_f<T>(s);
+}
+
+// ---------------------------------------------------------------- paged
+// One CTA per tile of 64 query rows of the new tokens.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) paged_kernel(const __grid_constant__ PagedArgs a) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + kTile, *V = K + kTile, *P = V + kTile;
+    __shared__ int page_s[kT];
+    const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status);
+    const TokenTile t = token_tile(a.cu, nullptr, a.n_seqs, a.T, TQ, blockIdx.x);
+    if (t.t0 >= t.n) return;
+    int kv, first;
+    if (!paged_seq(a, t.b, t.n, kv, first, threadIdx.x == 0)) return;
+    const int32_t* table = a.table + (size_t)t.b * a.max_pages;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    load_tile<T>(Q, [&](int r) -> const T* {
+        const int i = t.t0 + r / G;
+        return r < TQ * G && i < t.n ? view_row<T>(a.q, 0, hk * G + r % G, t.start + i) : nullptr;
+    });
+    float m[4], l[4], o[4][4];
+    int pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i, tok = t.t0 + r / G;
+        pos[i] = r < TQ * G && tok < t.n ? first + tok : -1;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+    }
+    const float sc = a.scale * kLog2e;
+    const int i0 = imax(0, first + t.t0), i1 = first + imin(t.t0 + TQ, t.n) - 1;
+    KeyBlocks kb = {0, 0, 0};
+    if (i1 >= 0) kb = key_blocks(i0, i1, kv, a.w, a.sinks, kT);
+    for (int n = 0; n < kb.n; ++n) {
+        const int c0 = key_block(kb, n) * kT;
+        __syncthreads();
+        if (threadIdx.x < kT) {
+            const int j = c0 + threadIdx.x;
+            const int page = j < kv ? page_of(table, a.max_pages, a.num_pages, a.page_shift, j) : -1;
+            page_s[threadIdx.x] = page;
+            if (page < 0 && j < kv && range_visible(i0, i1, j, j, a.w, a.sinks))
+                record_status(a.status, t.b, LF_ERR_BAD_PAGE);
+        }
+        __syncthreads();
+        const int in_page = (1 << a.page_shift) - 1;
+        load_tile<T>(K, [&](int r) -> const T* {
+            return page_s[r] >= 0 ? view_row<T>(a.k, page_s[r], hk, (c0 + r) & in_page) : nullptr;
+        });
+        load_tile<T>(V, [&](int r) -> const T* {
+            return page_s[r] >= 0 ? view_row<T>(a.v, page_s[r], hk, (c0 + r) & in_page) : nullptr;
+        });
+        __syncthreads();
+        float s[4][4];
+        tile_nt(s, Q, K, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j;
+                s[i][j] = page_s[c] >= 0 && key_visible(pos[i], c0 + c, a.w, a.sinks) ? s[i][j] * sc : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            const float mn = fmaxf(m[i], max16(mx));
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - base);
+                sum += p;
+                P[(4 * ty + i) * kLd + tx + 16 * j] = p;
+            }
+            m[i] = mn;
+            l[i] = l[i] * f + sum16(sum);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[i][c] *= f;
+        }
+        __syncwarp();
+        tile_nn(o, P, V, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i, tok = t.t0 + r / G, h = hk * G + r % G;
+        if (r >= TQ * G || tok >= t.n) continue;
+        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][c] *= inv;
+        store4(static_cast<T*>(a.out) + ((size_t)(t.start + tok) * a.Hq + h) * kD + 4 * tx, o[i]);
+    }
+}
+
+template <typename K>
+lf_status set_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
+               ? LF_OK : LF_ERR_CUDA;
+}
+
+template <typename K, typename A>
+lf_status launch(K kernel, dim3 grid, int tiles, const A& a, cudaStream_t stream) {
+    const size_t bytes = (size_t)tiles * kTile * sizeof(float);
+    lf_status st = set_smem(kernel, bytes);
+    if (st != LF_OK) return st;
+    kernel<<<grid, kThreads, bytes, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}
+
+template <typename T>
+lf_status forward_t(const WindowArgs& a, cudaStream_t stream) {
+    const int TQ = kT / a.heads_group();
+    return launch(forward_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 4, a, stream);
+}
+
+template <typename T>
+lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
+    const int TQ = kT / a.heads_group();
+    lf_status st = launch(dq_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 5, a, stream);
+    if (st == LF_OK)
+        st = launch(dkv_kernel<T, false>, dim3(token_slots(a.packed(), a.n_seqs, a.L, kT), a.Hkv), 6, a, stream);
+    if (st == LF_OK && a.sinks > 0) {
+        st = launch(dkv_kernel<T, true>,
+                    dim3(token_slots(a.packed(), a.n_seqs, a.L, a.chunk), a.Hkv, (a.sinks + kT - 1) / kT), 6, a, stream);
+        if (st == LF_OK) st = launch_sink_reduce(a, stream);
+    }
+    return st;
+}
+
+}  // namespace
+
+lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream) {
+    if (a.dtype == LF_F16) return forward_t<__half>(a, stream);
+    if (a.dtype == LF_BF16) return forward_t<__nv_bfloat16>(a, stream);
+    return forward_t<float>(a, stream);
+}
+
+lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream) {
+    if (a.dtype == LF_F16) return backward_t<__half>(a, stream);
+    if (a.dtype == LF_BF16) return backward_t<__nv_bfloat16>(a, stream);
+    return backward_t<float>(a, stream);
+}
+
+lf_status launch_sink_reduce(const WindowArgs& a, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.n_seqs * a.sinks, a.Hkv);
+    if (a.dtype == LF_F16) sink_reduce_kernel<__half><<<grid, 128, 0, stream>>>(a);
+    else if (a.dtype == LF_BF16) sink_reduce_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a);
+    else sink_reduce_kernel<float><<<grid, 128, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+}
+
+lf_status launch_paged_forward_simt(const PagedArgs& a, cudaStream_t stream) {
+    const dim3 grid(packed_slots(a.T, a.n_seqs, kT / a.heads_group()), a.Hkv);
+    if (a.dtype == LF_F16) return launch(paged_kernel<__half>, grid, 4, a, stream);
+    return launch(paged_kernel<__nv_bfloat16>, grid, 4, a, stream);
+}
+
+}  // namespace lf

@@ -8,6 +8,7 @@ library is missing this module raises instead of falling back to anything.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -30,6 +31,12 @@ LAYER_FIELDS = ("W_qkv_kgvg", "b_qkv_kgvg", "W_qg", "b_qg", "W_o", "b_o", "ln1_g
 class LayerWeights(ctypes.Structure):
     """lf_layer_weights of include/lf.h."""
     _fields_ = [("ffn_dim", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in LAYER_FIELDS]
+
+
+class Heads(ctypes.Structure):
+    """lf_heads of include/lf.h: a view of per-head rows of 64 elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong)]
 
 
 class LFError(RuntimeError):
@@ -96,6 +103,25 @@ def lib():
         L.lf_set_ffn_path.restype = st
         L.lf_get_ffn_path.argtypes = []
         L.lf_get_ffn_path.restype = i
+        f, ll, sz, hp = ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(Heads)
+        L.lf_window_attention_forward.argtypes = [hp] * 3 + [vp, vp] + [i] * 6 + [f, i, vp, vp, vp]
+        L.lf_window_attention_forward.restype = st
+        L.lf_window_attention_backward_workspace_bytes.argtypes = [i] * 7
+        L.lf_window_attention_backward_workspace_bytes.restype = sz
+        L.lf_window_attention_backward.argtypes = ([hp] * 3 + [vp] * 5 + [i] * 6 + [f, i, vp, sz, vp] + [hp] * 3)
+        L.lf_window_attention_backward.restype = st
+        L.lf_paged_cache_append.argtypes = [hp] * 4 + [vp] * 3 + [i] * 7 + [vp]
+        L.lf_paged_cache_append.restype = st
+        L.lf_paged_attention_workspace_bytes.argtypes = [i] * 9
+        L.lf_paged_attention_workspace_bytes.restype = sz
+        L.lf_paged_attention_forward.argtypes = [hp] * 3 + [vp] * 3 + [i] * 10 + [f, i, vp, sz, vp, vp]
+        L.lf_paged_attention_forward.restype = st
+        L.lf_layer_norm_forward.argtypes = [vp, ll, vp, vp, i, i, f, i, vp, vp, vp, vp]
+        L.lf_layer_norm_forward.restype = st
+        L.lf_layer_norm_backward_workspace_bytes.argtypes = [i, i]
+        L.lf_layer_norm_backward_workspace_bytes.restype = sz
+        L.lf_layer_norm_backward.argtypes = [vp, ll, vp, ll, vp, vp, vp, i, i, i, vp, sz, vp, vp, vp, vp]
+        L.lf_layer_norm_backward.restype = st
         _lib = L
     return _lib
 
@@ -364,3 +390,265 @@ def _encoder(fn_name, size_fn, x, local_mask, global_mask, layers, H, w, attn_sc
                                  _stream(stream), _ptr(out))
     _check(st, fn_name)
     return out
+
+
+# --------------------------------------------------------------------------
+# windowed causal attention with sinks, its paged form, layer norm
+# --------------------------------------------------------------------------
+@contextlib.contextmanager
+def _on(first, stream, *tensors):
+    """The device of `first` current and `stream` (default: that device's
+    current one) the stream that outputs and workspaces are allocated on."""
+    if not first.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors on different devices: %s and %s" % (first.device, t.device))
+    if stream is not None and stream.device != first.device:
+        raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, first.device))
+    with torch.cuda.device(first.device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _want(name, t, dtype=None, shape=None):
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _int32(**values):
+    for name, x in values.items():
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError("%s: %d is not an int32" % (name, x))
+
+
+def _heads(name, t, dtype=None, shape=None):
+    """lf_heads of [B, H, T, 64], or of packed [T, H, 64]."""
+    _want(name, t, dtype, shape)
+    if t.dim() not in (3, 4) or t.shape[-1] != 64:
+        raise ValueError("%s: expected [B, H, L, 64] or packed [T, H, 64], got %s" % (name, tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError("%s: the last dimension must be contiguous" % name)
+    if t.dim() == 3:
+        return ctypes.byref(Heads(t.data_ptr(), 0, t.stride(1), t.stride(0)))
+    return ctypes.byref(Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+
+
+def _window_shape(q, k, v, cu_seqlens, seq_lens):
+    """(packed, n_seqs, Hq, Hkv, L, shape of out, shape of lse)"""
+    packed = cu_seqlens is not None
+    if q.dim() != (3 if packed else 4):
+        raise ValueError("q: expected %s, got %s" % ("packed [T, H, 64]" if packed else "[B, H, L, 64]",
+                                                     tuple(q.shape)))
+    if packed:
+        _want("cu_seqlens", cu_seqlens, torch.int32)
+        if seq_lens is not None:
+            raise ValueError("give cu_seqlens or seq_lens, not both")
+        L, Hq, _ = q.shape
+        Hkv = k.shape[1]
+        _want("k", k, q.dtype, (L, Hkv, 64))
+        _want("v", v, q.dtype, (L, Hkv, 64))
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens: expected [n_seqs + 1]")
+        return True, cu_seqlens.numel() - 1, Hq, Hkv, L, (L, Hq * 64), (1, Hq, L)
+    B, Hq, L, _ = q.shape
+    Hkv = k.shape[1]
+    _want("k", k, q.dtype, (B, Hkv, L, 64))
+    _want("v", v, q.dtype, (B, Hkv, L, 64))
+    if seq_lens is not None:
+        _want("seq_lens", seq_lens, torch.int32, (B,))
+    return False, B, Hq, Hkv, L, (B, L, Hq * 64), (B, Hq, L)
+
+
+def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 0.125, cu_seqlens=None,
+                                seq_lens=None, out=None, lse=None, stream=None):
+    """Causal attention in which the query at position i sees the keys j <= i
+    with i - j <= w or j < sinks.  q [B, Hq, L, 64], k, v [B, Hkv, L, 64] (any
+    strides, last dimension contiguous), with seq_lens [B] int32 tokens per
+    row when padded; or packed q [T, Hq, 64], k, v [T, Hkv, 64] with
+    cu_seqlens [n + 1] int32.  Returns (out [B, L, Hq*64] or [T, Hq*64], lse
+    [B, Hq, L] or [1, Hq, T] float32, for the backward pass)."""
+    _int32(w=w, sinks=sinks)
+    packed, n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
+    with _on(q, stream, k, v, cu_seqlens, seq_lens, out, lse):
+        out = torch.empty(o_shape, dtype=q.dtype, device=q.device) if out is None else _want("out", out, q.dtype, o_shape)
+        lse = (torch.empty(l_shape, dtype=torch.float32, device=q.device) if lse is None
+               else _want("lse", lse, torch.float32, l_shape))
+        st = lib().lf_window_attention_forward(
+            _heads("q", q), _heads("k", k), _heads("v", v), _ptr(cu_seqlens), _ptr(seq_lens), n, Hq, Hkv, L, w, sinks,
+            scale, DTYPE_CODE.get(q.dtype, 99), _stream(stream), _ptr(out), _ptr(lse))
+    _check(st, "lf_window_attention_forward")
+    return out, lse
+
+
+def lf_window_attention_backward_workspace_bytes(packed: bool, n_seqs: int, Hq: int, Hkv: int, L: int, w: int,
+                                                 sinks: int) -> int:
+    return lib().lf_window_attention_backward_workspace_bytes(int(packed), n_seqs, Hq, Hkv, L, w, sinks)
+
+
+def lf_window_attention_backward(q, k, v, out, lse, dout, w: int, sinks: int = 0, scale: float = 0.125,
+                                 cu_seqlens=None, seq_lens=None, dq=None, dk=None, dv=None, workspace=None,
+                                 stream=None):
+    """Gradients of :func:`lf_window_attention_forward`: out and lse as it
+    returned them, dout like out (contiguous).  dq, dk, dv may be strided
+    views (of one gradient of a fused projection, say); without them they are
+    allocated like q, k, v, contiguous.  Returns (dq, dk, dv)."""
+    _int32(w=w, sinks=sinks)
+    packed, n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
+    _want("out", out, q.dtype, o_shape)
+    _want("dout", dout, q.dtype, o_shape)
+    _want("lse", lse, torch.float32, l_shape)
+    with _on(q, stream, k, v, out, lse, dout, cu_seqlens, seq_lens, dq, dk, dv, workspace):
+        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) if g is None else g
+                      for g, t in ((dq, q), (dk, k), (dv, v)))
+        need = lf_window_attention_backward_workspace_bytes(packed, n, Hq, Hkv, L, w, sinks)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        st = lib().lf_window_attention_backward(
+            _heads("q", q), _heads("k", k), _heads("v", v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_seqlens),
+            _ptr(seq_lens), n, Hq, Hkv, L, w, sinks, scale, DTYPE_CODE.get(q.dtype, 99), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream), _heads("dq", dq, q.dtype, q.shape),
+            _heads("dk", dk, q.dtype, k.shape), _heads("dv", dv, q.dtype, v.shape))
+    _check(st, "lf_window_attention_backward")
+    return dq, dk, dv
+
+
+def _paged_shape(new, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
+    """(n_seqs, T, Hkv, max_pages, num_pages, page_size)"""
+    if new.dim() != 3:
+        raise ValueError("expected packed [T, H, 64], got %s" % (tuple(new.shape),))
+    if k_cache.dim() != 4 or k_cache.shape[-1] != 64:
+        raise ValueError("k_cache: expected [num_pages, Hkv, page_size, 64], got %s" % (tuple(k_cache.shape),))
+    _want("k_cache", k_cache, new.dtype)
+    _want("v_cache", v_cache, new.dtype, k_cache.shape)
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [n_seqs, max_pages]")
+    n, max_pages = block_table.shape
+    _want("block_table", block_table, torch.int32)
+    _want("cu_seqlens", cu_seqlens, torch.int32, (n + 1,))
+    _want("kv_lens", kv_lens, torch.int32, (n,))
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    return n, new.shape[0], Hkv, max_pages, num_pages, page_size
+
+
+def lf_paged_cache_append(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, stream=None):
+    """Copy new tokens' k, v [T, Hkv, 64] (packed by cu_seqlens [n + 1]) to
+    the last positions of their sequences (kv_lens [n] positions in all) in
+    the paged cache k_cache, v_cache [num_pages, Hkv, page_size, 64] (any
+    strides) through block_table [n, max_pages] int32."""
+    n, T, Hkv, max_pages, num_pages, page_size = _paged_shape(k, k_cache, v_cache, block_table, cu_seqlens, kv_lens)
+    _want("k", k, None, (T, Hkv, 64))
+    _want("v", v, k.dtype, (T, Hkv, 64))
+    with _on(k, stream, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
+        st = lib().lf_paged_cache_append(
+            _heads("k", k), _heads("v", v), _heads("k_cache", k_cache), _heads("v_cache", v_cache),
+            _ptr(block_table), _ptr(cu_seqlens), _ptr(kv_lens), n, Hkv, T, max_pages, num_pages, page_size,
+            DTYPE_CODE.get(k.dtype, 99), _stream(stream))
+    _check(st, "lf_paged_cache_append")
+
+
+def lf_paged_attention_workspace_bytes(n_seqs: int, Hq: int, Hkv: int, T: int, max_q_len: int, max_pages: int,
+                                       page_size: int, w: int, sinks: int) -> int:
+    return lib().lf_paged_attention_workspace_bytes(n_seqs, Hq, Hkv, T, max_q_len, max_pages, page_size, w, sinks)
+
+
+def lf_paged_attention_forward(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len: int,
+                               w: int = (1 << 31) - 1, sinks: int = 0, scale: float = 0.125, out=None,
+                               workspace=None, stream=None):
+    """Windowed causal attention of new tokens q [T, Hq, 64] (packed by
+    cu_seqlens, none of the sequences longer than max_q_len) over the paged
+    cache, which holds their own keys and values already
+    (:func:`lf_paged_cache_append`).  Returns out [T, Hq*64]."""
+    n, T, Hkv, max_pages, num_pages, page_size = _paged_shape(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens)
+    _int32(w=w, sinks=sinks, max_q_len=max_q_len)
+    Hq = q.shape[1]
+    with _on(q, stream, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, workspace):
+        out = (torch.empty(T, Hq * 64, dtype=q.dtype, device=q.device) if out is None
+               else _want("out", out, q.dtype, (T, Hq * 64)))
+        need = lf_paged_attention_workspace_bytes(n, Hq, Hkv, T, max_q_len, max_pages, page_size, w, sinks)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        st = lib().lf_paged_attention_forward(
+            _heads("q", q), _heads("k_cache", k_cache), _heads("v_cache", v_cache), _ptr(block_table),
+            _ptr(cu_seqlens), _ptr(kv_lens), n, Hq, Hkv, T, max_q_len, max_pages, num_pages, page_size, w, sinks,
+            scale, DTYPE_CODE.get(q.dtype, 99), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream), _ptr(out))
+    _check(st, "lf_paged_attention_forward")
+    return out
+
+
+def _rows(name, t):
+    """(pointer, rows, N, row stride) of [..., N]: contiguous, or 2-D with a
+    contiguous last dimension."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() == 0:
+        raise ValueError("%s: expected [..., N]" % name)
+    N = t.shape[-1]
+    rows = t.numel() // N if N else 0
+    if t.dim() == 2 and (t.stride(1) == 1 or N == 1) and not t.is_contiguous():
+        return ctypes.c_void_p(t.data_ptr()), rows, N, t.stride(0)
+    if not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous tensor, or a 2-D one with a row stride" % name)
+    return ctypes.c_void_p(t.data_ptr()), rows, N, N
+
+
+def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x [..., N]; gamma, beta [N] float32 or None.
+    Returns (y, mean, rstd), mean and rstd [rows] float32 for the backward
+    pass."""
+    with _on(x, stream, gamma, beta, out, mean, rstd):
+        px, rows, N, stride = _rows("x", x)
+        for name, t in (("gamma", gamma), ("beta", beta)):
+            if t is not None:
+                _want(name, t, torch.float32, (N,))
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else _want("out", out, x.dtype, x.shape)
+        mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) if t is None
+                      else _want(name, t, torch.float32, (rows,)) for name, t in (("mean", mean), ("rstd", rstd)))
+        st = lib().lf_layer_norm_forward(px, stride, _ptr(gamma), _ptr(beta), rows, N, eps,
+                                         DTYPE_CODE.get(x.dtype, 99), _stream(stream), _ptr(out), _ptr(mean),
+                                         _ptr(rstd))
+    _check(st, "lf_layer_norm_forward")
+    return out, mean, rstd
+
+
+def lf_layer_norm_backward_workspace_bytes(rows: int, N: int) -> int:
+    return lib().lf_layer_norm_backward_workspace_bytes(rows, N)
+
+
+def lf_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, param_grads: bool = True,
+                           workspace=None, stream=None):
+    """Gradients of :func:`lf_layer_norm_forward` (mean, rstd as it returned
+    them).  Returns (dx, dgamma, dbeta); with param_grads False only those of
+    dgamma, dbeta that were passed in are written."""
+    with _on(x, stream, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace):
+        px, rows, N, xs = _rows("x", x)
+        pdy, _, _, dys = _rows("dy", _want("dy", dy, x.dtype, x.shape))
+        if gamma is not None:
+            _want("gamma", gamma, torch.float32, (N,))
+        _want("mean", mean, torch.float32, (rows,))
+        _want("rstd", rstd, torch.float32, (rows,))
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else _want("dx", dx, x.dtype, x.shape)
+        if param_grads:
+            dgamma, dbeta = (torch.empty(N, dtype=torch.float32, device=x.device) if t is None else t
+                             for t in (dgamma, dbeta))
+        for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
+            if t is not None:
+                _want(name, t, torch.float32, (N,))
+        if workspace is None and (dgamma is not None or dbeta is not None):
+            workspace = torch.empty(max(256, lf_layer_norm_backward_workspace_bytes(rows, N)), dtype=torch.uint8,
+                                    device=x.device)
+        st = lib().lf_layer_norm_backward(
+            pdy, dys, px, xs, _ptr(gamma), _ptr(mean), _ptr(rstd), rows, N, DTYPE_CODE.get(x.dtype, 99),
+            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _stream(stream), _ptr(dx), _ptr(dgamma), _ptr(dbeta))
+    _check(st, "lf_layer_norm_backward")
+    return dx, dgamma, dbeta
