@@ -45,6 +45,7 @@ inline size_t sink_slots(const WindowArgs& a) {
 
 lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream);
 lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream);
+lf_status launch_window_forward_tc(const WindowArgs& a, cudaStream_t stream);   // 16-bit
 lf_status launch_sink_reduce(const WindowArgs& a, cudaStream_t stream);
 
 // ---- paged cache ----
@@ -84,7 +85,7 @@ __device__ __forceinline__ void check_lengths(const int32_t* cu, const int32_t* 
     }
 }
 lf_status launch_paged_append(const PagedArgs& a, cudaStream_t stream);
-lf_status launch_paged_forward_simt(const PagedArgs& a, cudaStream_t stream);
+lf_status launch_paged_forward_tc(const PagedArgs& a, cudaStream_t stream);
 
 // ---- layer norm ----
 struct NormArgs {

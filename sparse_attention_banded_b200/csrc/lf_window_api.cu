@@ -126,7 +126,8 @@ lf_status lf_window_attention_forward(const lf_heads* q, const lf_heads* k, cons
     a.out = out;
     a.lse = lse;
     a.status = d->status;
-    return launch_window_forward_simt(a, (cudaStream_t)stream);
+    return dtype == LF_F32 ? launch_window_forward_simt(a, (cudaStream_t)stream)
+                           : launch_window_forward_tc(a, (cudaStream_t)stream);
 }
 
 size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int Hq, int Hkv, int L, int w, int sinks) {
@@ -252,7 +253,7 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
     a.out = out;
     a.status = d->status;
     a.workspace = workspace;
-    return launch_paged_forward_simt(a, (cudaStream_t)stream);
+    return launch_paged_forward_tc(a, (cudaStream_t)stream);
 }
 
 lf_status lf_layer_norm_forward(const void* x, long long x_stride, const float* gamma, const float* beta, int rows,

@@ -1,5 +1,5 @@
-// Windowed causal attention with sinks on the CUDA cores: forward, backward
-// and the paged form, for every dtype (fp32 arithmetic throughout).
+// Windowed causal attention with sinks on the CUDA cores: forward (fp32) and
+// backward, fp32 arithmetic throughout.
 //
 //   forward   one CTA per tile of 64 query rows (64 / G tokens times the G
 //             query heads of a key/value head), online softmax over blocks
@@ -406,99 +406,6 @@ __global__ void __launch_bounds__(128) sink_reduce_kernel(const __grid_constant_
     const_cast<T*>(view_row<T>(v, a.cu ? 0 : b, hk, start + key))[e & (kD - 1)] = from_f<T>(s);
 }
 
-// ---------------------------------------------------------------- paged
-// One CTA per tile of 64 query rows of the new tokens.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) paged_kernel(const __grid_constant__ PagedArgs a) {
-    extern __shared__ float sm[];
-    float *Q = sm, *K = Q + kTile, *V = K + kTile, *P = V + kTile;
-    __shared__ int page_s[kT];
-    const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
-    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status);
-    const TokenTile t = token_tile(a.cu, nullptr, a.n_seqs, a.T, TQ, blockIdx.x);
-    if (t.t0 >= t.n) return;
-    int kv, first;
-    if (!paged_seq(a, t.b, t.n, kv, first, threadIdx.x == 0)) return;
-    const int32_t* table = a.table + (size_t)t.b * a.max_pages;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_tile<T>(Q, [&](int r) -> const T* {
-        const int i = t.t0 + r / G;
-        return r < TQ * G && i < t.n ? view_row<T>(a.q, 0, hk * G + r % G, t.start + i) : nullptr;
-    });
-    float m[4], l[4], o[4][4];
-    int pos[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i, tok = t.t0 + r / G;
-        pos[i] = r < TQ * G && tok < t.n ? first + tok : -1;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-    }
-    const float sc = a.scale * kLog2e;
-    const int i0 = imax(0, first + t.t0), i1 = first + imin(t.t0 + TQ, t.n) - 1;
-    KeyBlocks kb = {0, 0, 0};
-    if (i1 >= 0) kb = key_blocks(i0, i1, kv, a.w, a.sinks, kT);
-    for (int n = 0; n < kb.n; ++n) {
-        const int c0 = key_block(kb, n) * kT;
-        __syncthreads();
-        if (threadIdx.x < kT) {
-            const int j = c0 + threadIdx.x;
-            const int page = j < kv ? page_of(table, a.max_pages, a.num_pages, a.page_shift, j) : -1;
-            page_s[threadIdx.x] = page;
-            if (page < 0 && j < kv && range_visible(i0, i1, j, j, a.w, a.sinks))
-                record_status(a.status, t.b, LF_ERR_BAD_PAGE);
-        }
-        __syncthreads();
-        const int in_page = (1 << a.page_shift) - 1;
-        load_tile<T>(K, [&](int r) -> const T* {
-            return page_s[r] >= 0 ? view_row<T>(a.k, page_s[r], hk, (c0 + r) & in_page) : nullptr;
-        });
-        load_tile<T>(V, [&](int r) -> const T* {
-            return page_s[r] >= 0 ? view_row<T>(a.v, page_s[r], hk, (c0 + r) & in_page) : nullptr;
-        });
-        __syncthreads();
-        float s[4][4];
-        tile_nt(s, Q, K, ty, tx);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = tx + 16 * j;
-                s[i][j] = page_s[c] >= 0 && key_visible(pos[i], c0 + c, a.w, a.sinks) ? s[i][j] * sc : -INFINITY;
-                mx = fmaxf(mx, s[i][j]);
-            }
-            const float mn = fmaxf(m[i], max16(mx));
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m[i] - base);
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = exp2f(s[i][j] - base);
-                sum += p;
-                P[(4 * ty + i) * kLd + tx + 16 * j] = p;
-            }
-            m[i] = mn;
-            l[i] = l[i] * f + sum16(sum);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[i][c] *= f;
-        }
-        __syncwarp();
-        tile_nn(o, P, V, ty, tx);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i, tok = t.t0 + r / G, h = hk * G + r % G;
-        if (r >= TQ * G || tok >= t.n) continue;
-        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[i][c] *= inv;
-        store4(static_cast<T*>(a.out) + ((size_t)(t.start + tok) * a.Hq + h) * kD + 4 * tx, o[i]);
-    }
-}
-
 template <typename K>
 lf_status set_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
@@ -537,8 +444,6 @@ lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
 }  // namespace
 
 lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream) {
-    if (a.dtype == LF_F16) return forward_t<__half>(a, stream);
-    if (a.dtype == LF_BF16) return forward_t<__nv_bfloat16>(a, stream);
     return forward_t<float>(a, stream);
 }
 
@@ -554,12 +459,6 @@ lf_status launch_sink_reduce(const WindowArgs& a, cudaStream_t stream) {
     else if (a.dtype == LF_BF16) sink_reduce_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a);
     else sink_reduce_kernel<float><<<grid, 128, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
-}
-
-lf_status launch_paged_forward_simt(const PagedArgs& a, cudaStream_t stream) {
-    const dim3 grid(packed_slots(a.T, a.n_seqs, kT / a.heads_group()), a.Hkv);
-    if (a.dtype == LF_F16) return launch(paged_kernel<__half>, grid, 4, a, stream);
-    return launch(paged_kernel<__nv_bfloat16>, grid, 4, a, stream);
 }
 
 }  // namespace lf
