@@ -29,6 +29,16 @@ static __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     return d;
 }
 
+static __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // 2^x for a pair on the FMA/ALU pipes, to take load off the MUFU unit
 // (16 results per clock per SM).  Cody-Waite reduction x = n + f with
 // n = round(x) (|f| <= 1/2, via the 1.5 * 2^23 rounding constant), then a

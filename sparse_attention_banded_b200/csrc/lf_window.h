@@ -43,9 +43,10 @@ inline size_t sink_slots(const WindowArgs& a) {
     return (size_t)a.n_seqs + token_slots(a.packed(), a.n_seqs, a.L, a.chunk);
 }
 
-lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream);
-lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream);
+lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream);   // fp32
+lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream);  // fp32
 lf_status launch_window_forward_tc(const WindowArgs& a, cudaStream_t stream);   // 16-bit
+lf_status launch_window_backward_tc(const WindowArgs& a, cudaStream_t stream);  // 16-bit
 lf_status launch_sink_reduce(const WindowArgs& a, cudaStream_t stream);
 
 // ---- paged cache ----

@@ -170,7 +170,8 @@ lf_status lf_window_attention_backward(const lf_heads* q, const lf_heads* k, con
     a.delta = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256((size_t)B * Hq * L * sizeof(float)));
     a.status = d->status;
-    return launch_window_backward_simt(a, (cudaStream_t)stream);
+    return dtype == LF_F32 ? launch_window_backward_simt(a, (cudaStream_t)stream)
+                           : launch_window_backward_tc(a, (cudaStream_t)stream);
 }
 
 lf_status lf_paged_cache_append(const lf_heads* k_new, const lf_heads* v_new, const lf_heads* k_cache,

@@ -1,0 +1,598 @@
+// Windowed causal attention with sinks, backward, on the sm_100a tensor cores
+// (fp16 / bf16).  P is recomputed from the saved log-sum-exp, so no pass over
+// the keys needs a running maximum:
+//     P = 2^(S - lse),  dP = dO V^T,  dS = P (dP - delta),  delta = rowsum(dO * out)
+//
+// dq_kernel     one CTA per 128 query rows (128 / G tokens x G heads), over
+//               the blocks of 64 keys it sees:  dQ += dS K.  Writes delta.
+// dkv_kernel    one CTA per 128 keys, over the tiles of 64 query rows that
+//               hold them in their window, all G heads of the group:
+//                   dV += P^T dO,  dK += dS^T Q
+//               with S^T = K Q^T and dP^T = V dO^T, so that P^T and dS^T land
+//               with keys on the tensor-memory lanes, ready as A operands.
+//               Other CTAs of the same launch take the sink keys over a chunk
+//               of the queries outside their window and leave fp32 partials.
+// Two kernels compute S and dP twice (7 products instead of 5) but every sum
+// has one owner: no atomics, the results repeat bit for bit, and neither dQ
+// nor dK, dV ever leaves tensor memory unfinished.
+//
+// The 8 math warps split a tile's columns in halves (two threads a row), the
+// 16-bit P or dS of a half overwriting the first 16 columns of that half's
+// scores.  256 tensor-memory columns a CTA, two CTAs per SM: one's products
+// run under the other's exponentials.  P and dS are rounded to the storage
+// type, the MMA's operand type; accumulators are fp32, rounded once.
+//
+// Rows of other sequences (or of no token) that a tile's loads bring along
+// are zeroed in shared memory where they are a product's inner dimension:
+// their P is 0, but 0 * NaN is not.
+#include <atomic>
+
+#include "lf_tc_tiles.cuh"
+
+namespace lf {
+namespace {
+
+using namespace sm100;
+
+constexpr int kD = 64;
+constexpr int kStages = 3;
+constexpr int kMathWarps = 8;
+constexpr int kThreads = (kMathWarps + 2) * 32;  // warp 8: TMA, warp 9: MMA
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kBig = 128 * kD * 2, kSmall = 64 * kD * 2;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Shared memory: two stationary tiles (128 rows), kStages pairs of moving
+// tiles (64 rows), per-row constants, barriers.
+constexpr uint32_t kOffB = 2 * kBig;                       // moving: stage s, tile 0 / 1
+constexpr uint32_t kOffRow = kOffB + kStages * 2 * kSmall; // floats
+constexpr uint32_t kRowFloats = kStages * 128;
+constexpr uint32_t kOffBar = kOffRow + kRowFloats * 4;
+constexpr uint32_t kBars = 1 + 2 * kStages + 6;
+constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;      // + alignment slack
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+
+struct Maps {
+    CUtensorMap q, k, v, dout;  // stationary or moving boxes, per kernel
+};
+
+struct Ctx {
+    uint8_t* smem;
+    uint64_t *a_full, *b_full, *b_empty, *s_full, *free_, *ready, *done, *drain;
+    volatile int* abort_flag;
+    uint32_t tmem;
+};
+
+// Barriers and tensor memory.  `ready_count`: arrivals of a math step.
+__device__ __forceinline__ Ctx setup(uint8_t* smem, int warp, int lane) {
+    Ctx c;
+    c.smem = smem;
+    c.a_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    c.b_full = c.a_full + 1;
+    c.b_empty = c.b_full + kStages;
+    c.s_full = c.b_empty + kStages;
+    c.free_ = c.s_full + 1;
+    c.ready = c.free_ + 1;  // [2]
+    c.done = c.ready + 2;
+    c.drain = c.done + 1;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+    c.abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+    if (threadIdx.x == 0) {
+        mbar_init(c.a_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&c.b_full[s], 1);
+            mbar_init(&c.b_empty[s], 1);
+        }
+        mbar_init(c.s_full, 1);
+        mbar_init(c.free_, kMathWarps);
+        mbar_init(&c.ready[0], kMathWarps);
+        mbar_init(&c.ready[1], kMathWarps);
+        mbar_init(c.done, 1);
+        mbar_init(c.drain, 1);
+        *c.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMathWarps + 1) {
+        tmem_alloc(slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    c.tmem = *slot;
+    return c;
+}
+
+__device__ __forceinline__ void finish(const Ctx& c, int warp, int* status) {
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *c.abort_flag) record_status(status, 0, LF_ERR_DEVICE_TIMEOUT);
+    if (warp == kMathWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc(c.tmem, kTmemCols);
+    }
+}
+
+// Wind-down after an abort: issued copies land, issued MMAs end.
+__device__ __forceinline__ void drain_loads(const Ctx& c, int issued) {
+    volatile int never = 0;
+    mbar_wait(c.a_full, 0, &never, 200000000ull);
+    for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+        mbar_wait(&c.b_full[j % kStages], (j / kStages) & 1, &never, 200000000ull);
+}
+__device__ __forceinline__ void drain_mmas(const Ctx& c) {
+    volatile int never = 0;
+    tc_commit(c.drain);
+    mbar_wait(c.drain, 0, &never, 200000000ull);
+}
+
+// D = A B^T, both 64 wide and K-major in shared memory (M 128, N 64).
+template <typename T>
+__device__ __forceinline__ void mma_nt(uint32_t d, uint32_t a_smem, uint32_t b_smem) {
+    constexpr uint32_t id = idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 0);
+    const uint64_t da = desc_sw128(a_smem), db = desc_sw128(b_smem);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f16_ss(d, da + k * 2, db + k * 2, id, k > 0);
+}
+// D += A B: A (128 x 64, 16-bit) in tensor memory, its halves 32 columns
+// apart; B 64 x 64 in shared memory.
+template <typename T>
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a_tmem, uint32_t b_smem, bool accumulate) {
+    constexpr uint32_t id = idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 1);
+    const uint64_t db = desc_sw128(b_smem, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        mma_f16_ts(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, db + k * (2048 >> 4), id, accumulate || k > 0);
+}
+
+// exp2 of a pair; in a tile without masked scores a third run on the FMA pipe.
+__device__ __forceinline__ float2 exp_pair(float2 v, bool poly) {
+    return poly ? exp2_poly2(v) : make_float2(ex2(v.x), ex2(v.y));
+}
+
+// Zero the rows [from, 64) of a 64-row tile (256 math threads).
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
+    const int row = threadIdx.x >> 2;
+    if (row >= from) {
+        uint4* z = reinterpret_cast<uint4*>(tile + row * 128 + (threadIdx.x & 3) * 32);
+        z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+__device__ __forceinline__ uint8_t* smem_base() {
+    extern __shared__ uint8_t raw[];
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+}
+
+// ---------------------------------------------------------------- dQ
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs a) {
+    uint8_t* smem = smem_base();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int G = a.Hq / a.Hkv, TQ = 128 / G, hk = blockIdx.y;
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status);
+    // long rows of a causal sequence first
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, gridDim.x - 1 - blockIdx.x);
+    if (t.t0 >= t.rows) return;
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2;  // math warps: row, column half
+    const int tok = t.t0 + r / G, head = hk * G + r % G;
+    const bool stored = warp < kMathWarps && r < TQ * G && tok < t.rows;
+    const bool live = stored && tok < t.n;
+    T* dq = view_row<T>(a.dq, t.batch, head, t.start + tok) + half * 32;
+    if (t.t0 >= t.n) {  // padding
+        if (stored)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(dq)[c] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const int i0 = t.t0, i1 = imin(t.t0 + TQ, t.n) - 1;
+    const KeyBlocks kb = key_blocks(i0, i1, t.n, a.w, a.sinks, 64);
+    const Ctx c = setup(smem, warp, lane);
+    const uint32_t tmS = c.tmem, tmP = c.tmem + 128, tmQ = c.tmem + 192;
+    float* row_s = reinterpret_cast<float*>(smem + kOffRow);
+
+    if (warp == kMathWarps) {
+        // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            mbar_arrive_expect_tx(c.a_full, 2 * (uint32_t)(TQ * G) * kD * 2);
+            tma_load_4d(smem, &maps.q, c.a_full, 0, hk * G, t.start + t.t0, t.batch);
+            tma_load_4d(smem + kBig, &maps.dout, c.a_full, 0, hk * G, t.start + t.t0, t.batch);
+        }
+        bool ok = true;
+        int j = 0;
+        for (; j < kb.n; ++j) {
+            const int s = j % kStages;
+            ok = warp_wait(&c.b_empty[s], ((j / kStages) & 1) ^ 1, c.abort_flag);
+            if (!ok) break;
+            if (lane == 0) {
+                uint8_t* d = smem + kOffB + s * 2 * kSmall;
+                const int row = t.start + key_block(kb, j) * 64;
+                mbar_arrive_expect_tx(&c.b_full[s], 2 * kSmall);
+                tma_load_4d(d, &maps.k, &c.b_full[s], 0, hk, row, t.batch);
+                tma_load_4d(d + kSmall, &maps.v, &c.b_full[s], 0, hk, row, t.batch);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) drain_loads(c, j);
+    } else if (warp == kMathWarps + 1) {
+        // ------------------------------------------------------------ MMA
+        // S alternates between two buffers; S and dP of block j + 1 are issued
+        // as soon as the math warps have read dP of block j, before dQ of j.
+        const uint32_t b0 = smem_u32(smem + kOffB);
+        bool ok = warp_wait(c.a_full, 0, c.abort_flag);
+        auto scores = [&](int j) -> bool {
+            const int s = j % kStages;
+            if (!warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag)) return false;
+            if (j > 0 && !warp_wait(c.free_, (j - 1) & 1, c.abort_flag)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_nt<T>(tmS + (j & 1) * 64, smem_u32(smem), b0 + s * 2 * kSmall);
+                mma_nt<T>(tmP, smem_u32(smem + kBig), b0 + s * 2 * kSmall + kSmall);
+                tc_commit(c.s_full);
+            }
+            __syncwarp();
+            return true;
+        };
+        ok = ok && scores(0);
+        for (int j = 0; j < kb.n && ok; ++j) {
+            if (j + 1 < kb.n) ok = scores(j + 1);
+            ok = ok && warp_wait(&c.ready[j & 1], (j >> 1) & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_tn<T>(tmQ, tmS + (j & 1) * 64, b0 + (j % kStages) * 2 * kSmall, j > 0);
+                tc_commit(&c.b_empty[j % kStages]);
+                if (j == kb.n - 1) tc_commit(c.done);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) drain_mmas(c);
+    } else {
+        // ------------------------------------------------------------ math
+        // delta: two threads a row, 32 products each
+        float part = 0.0f, nlse = 0.0f;
+        const size_t at = ((size_t)t.batch * a.Hq + head) * a.L + t.start + tok;
+        if (live) {
+            const size_t off = (((size_t)t.batch * a.L + t.start + tok) * a.Hq + head) * kD + half * 32;
+            const uint4* po = reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + off);
+            const uint4* pd = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + off);
+            nlse = -a.lse[at] * kLog2e;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint4 x = po[u], y = pd[u];
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = Pair<T>::unpack(xs[e]), g = Pair<T>::unpack(ys[e]);
+                    part = fmaf(f.x, g.x, fmaf(f.y, g.y, part));
+                }
+            }
+        }
+        row_s[half * 128 + r] = part;
+        named_bar_sync(1, kMathWarps * 32);
+        const float ndelta = -(row_s[r] + row_s[128 + r]);
+        if (live && half == 0) a.delta[at] = -ndelta;
+
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const float sc = a.scale * kLog2e;
+        const float2 sc2 = make_float2(sc, sc), nl2 = make_float2(nlse, nlse), nd2 = make_float2(ndelta, ndelta);
+        bool ok = true;
+        for (int j = 0; j < kb.n; ++j) {
+            const int c0 = key_block(kb, j) * 64;
+            const uint32_t tS = tmS + lane_off + (j & 1) * 64 + half * 32;
+            const uint32_t bits = live ? (uint32_t)(visible_bits(tok, c0, t.n, a.w, a.sinks) >> (32 * half)) : 0u;
+            const bool full = __all_sync(0xffffffffu, bits == ~0u);
+            ok = warp_wait(c.s_full, j & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            float x[32], y[32];
+            tmem_ld32f(tS, x);
+            tmem_ld32f(tmP + lane_off + half * 32, y);
+            tmem_ld_wait();
+            regs_ready<32>(x);
+            regs_ready<32>(y);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.free_);
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float2 p = exp_pair(ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nl2), full && e % 3 == 2);
+                float2 d = fmul2(p, fadd2(make_float2(y[2 * e], y[2 * e + 1]), nd2));
+                if (!full) {
+                    d.x = (bits >> (2 * e)) & 1 ? d.x : 0.0f;
+                    d.y = (bits >> (2 * e + 1)) & 1 ? d.y : 0.0f;
+                }
+                pk[e] = Pair<T>::pack(d.x, d.y);
+            }
+            tmem_st16(tS, pk);
+            if (c0 + 64 > t.n) {  // keys past the sequence
+                zero_rows(smem + kOffB + (j % kStages) * 2 * kSmall, t.n - c0);
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.ready[j & 1]);
+        }
+        if (ok && warp_wait(c.done, 0, c.abort_flag)) {
+            tc_fence_after();
+            float o[32];
+            tmem_ld32f(tmQ + lane_off + half * 32, o);
+            tmem_ld_wait();
+            regs_ready<32>(o);
+            if (live) store_row32(dq, o, a.scale);
+            else if (stored)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(dq)[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    finish(c, warp, a.status);
+}
+
+// ---------------------------------------------------------------- dK, dV
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs a, int sink_slots, int sink_items) {
+    uint8_t* smem = smem_base();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int G = a.Hq / a.Hkv, TQ = 64 / G, hk = blockIdx.y;
+    // the sink chunks come first: they are the longest items
+    const bool sink = (int)blockIdx.x < sink_items;
+    const int slot = sink ? blockIdx.x % sink_slots : blockIdx.x - sink_items;
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, sink ? a.chunk : 128, slot);
+    if (t.t0 >= (sink ? t.n : t.rows)) return;
+    const int c0 = sink ? (int)(blockIdx.x / sink_slots) * 128 : t.t0;  // first key
+    int q0 = c0, q1 = (int)min((long long)t.n, (long long)c0 + 128 + a.w);  // query tokens
+    if (sink) {
+        q0 = imax(t.t0, imin(c0, t.n) + a.w + 1);
+        q1 = imin(t.t0 + a.chunk, t.n);
+    }
+    const int n_keys = sink ? imin(a.sinks, t.n) : t.n;
+    const int nq = q1 > q0 ? (q1 - q0 + TQ - 1) / TQ : 0;
+
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2, key = c0 + r;
+    // where this thread's half rows of dK and dV go: the fp32 partials of a
+    // sink key, or the outputs
+    const int n_sink = imin(a.sinks, t.n);
+    float* part = nullptr;
+    T *dk = nullptr, *dv = nullptr;
+    if (warp < kMathWarps) {
+        if (key < n_sink) {
+            part = a.part + (((size_t)(sink ? a.n_seqs + slot : t.b) * a.Hkv + hk) * a.sinks + key) * 2 * kD + half * 32;
+        } else if (!sink && key < t.rows) {
+            dk = view_row<T>(a.dk, t.batch, hk, t.start + key) + half * 32;
+            dv = view_row<T>(a.dv, t.batch, hk, t.start + key) + half * 32;
+        }
+    }
+    if (nq == 0) {  // padding, or a chunk inside every window
+        if (part) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                reinterpret_cast<float4*>(part)[u] = reinterpret_cast<float4*>(part + kD)[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (dk) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                reinterpret_cast<uint4*>(dk)[u] = reinterpret_cast<uint4*>(dv)[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    if (TQ * G < 64 && warp < kMathWarps) {  // rows no load ever writes
+        for (int s = 0; s < 2 * kStages; ++s) zero_rows(smem + kOffB + s * kSmall, TQ * G);
+        fence_proxy_async_smem();
+    }
+    const Ctx c = setup(smem, warp, lane);
+    const uint32_t tmS = c.tmem, tmP = c.tmem + 64, tmV = c.tmem + 128, tmK = c.tmem + 192;
+    float* row_s = reinterpret_cast<float*>(smem + kOffRow);  // [stage][-lse log2e, -delta][64]
+
+    if (warp == kMathWarps) {
+        // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            mbar_arrive_expect_tx(c.a_full, 2 * kBig);
+            tma_load_4d(smem, &maps.k, c.a_full, 0, hk, t.start + c0, t.batch);
+            tma_load_4d(smem + kBig, &maps.v, c.a_full, 0, hk, t.start + c0, t.batch);
+        }
+        bool ok = true;
+        int j = 0;
+        for (; j < nq; ++j) {
+            const int s = j % kStages, qt = q0 + j * TQ;
+            // this lane's two rows
+            float nl[2], nd[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int row = lane + 32 * u, tok = qt + row / G;
+                const bool live = row < TQ * G && tok < q1;
+                const size_t at = ((size_t)t.batch * a.Hq + hk * G + row % G) * a.L + t.start + tok;
+                nl[u] = live ? -a.lse[at] * kLog2e : 0.0f;
+                nd[u] = live ? -a.delta[at] : 0.0f;
+            }
+            ok = warp_wait(&c.b_empty[s], ((j / kStages) & 1) ^ 1, c.abort_flag);
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                row_s[s * 128 + lane + 32 * u] = nl[u];
+                row_s[s * 128 + 64 + lane + 32 * u] = nd[u];
+            }
+            __syncwarp();
+            if (lane == 0) {
+                uint8_t* d = smem + kOffB + s * 2 * kSmall;
+                mbar_arrive_expect_tx(&c.b_full[s], 2 * (uint32_t)(TQ * G) * kD * 2);
+                tma_load_4d(d, &maps.q, &c.b_full[s], 0, hk * G, t.start + qt, t.batch);
+                tma_load_4d(d + kSmall, &maps.dout, &c.b_full[s], 0, hk * G, t.start + qt, t.batch);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) drain_loads(c, j);
+    } else if (warp == kMathWarps + 1) {
+        // ------------------------------------------------------------ MMA
+        const uint32_t b0 = smem_u32(smem + kOffB);
+        bool ok = warp_wait(c.a_full, 0, c.abort_flag);
+        for (int j = 0; j < nq && ok; ++j) {
+            const int s = j % kStages;
+            const uint32_t bq = b0 + s * 2 * kSmall, bo = bq + kSmall;
+            ok = warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_nt<T>(tmS, smem_u32(smem), bq);
+                mma_nt<T>(tmP, smem_u32(smem + kBig), bo);
+                tc_commit(c.s_full);
+            }
+            __syncwarp();
+            ok = warp_wait(&c.ready[0], j & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                mma_tn<T>(tmV, tmS, bo, j > 0);
+                mma_tn<T>(tmK, tmP, bq, j > 0);
+                tc_commit(&c.b_empty[s]);
+                if (j == nq - 1) tc_commit(c.done);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) drain_mmas(c);
+    } else {
+        // ------------------------------------------------------------ math
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmS + lane_off + half * 32, tP = tmP + lane_off + half * 32;
+        const float sc = a.scale * kLog2e;
+        const float2 sc2 = make_float2(sc, sc);
+        bool ok = true;
+        for (int j = 0; j < nq; ++j) {
+            const int s = j % kStages, qt = q0 + j * TQ;
+            // columns (query rows) that see this thread's key: tokens from
+            // the key on to the window's end, or past it for a sink
+            unsigned long long vis = 0;
+            if (key < n_keys) {
+                const int past = iclamp(key + a.w + 1 - qt, 0, 64) * G;
+                vis = low_bits64(iclamp(q1 - qt, 0, TQ) * G);
+                vis &= sink ? ~low_bits64(past) : low_bits64(past) & ~low_bits64(iclamp(key - qt, 0, 64) * G);
+            }
+            const uint32_t bits = (uint32_t)(vis >> (32 * half));
+            const bool full = __all_sync(0xffffffffu, bits == ~0u);
+            ok = warp_wait(c.s_full, j & 1, c.abort_flag) && warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            float x[32], y[32];
+            tmem_ld32f(tS, x);
+            tmem_ld32f(tP, y);
+            const float4* nl4 = reinterpret_cast<const float4*>(row_s + s * 128 + half * 32);
+            const float4* nd4 = nl4 + 16;
+            tmem_ld_wait();
+            regs_ready<32>(x);
+            regs_ready<32>(y);
+            uint32_t pp[16], pd[16];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float4 nl = nl4[u], nd = nd4[u];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = 2 * u + h;
+                    const float2 l2 = h ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
+                    const float2 d2 = h ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y);
+                    float2 p = exp_pair(ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, l2), full && e % 3 == 2);
+                    float2 d = fmul2(p, fadd2(make_float2(y[2 * e], y[2 * e + 1]), d2));
+                    if (!full) {
+                        const bool b0 = (bits >> (2 * e)) & 1, b1 = (bits >> (2 * e + 1)) & 1;
+                        p = make_float2(b0 ? p.x : 0.0f, b1 ? p.y : 0.0f);
+                        d = make_float2(b0 ? d.x : 0.0f, b1 ? d.y : 0.0f);
+                    }
+                    pp[e] = Pair<T>::pack(p.x, p.y);
+                    pd[e] = Pair<T>::pack(d.x, d.y);
+                }
+            }
+            tmem_st16(tS, pp);
+            tmem_st16(tP, pd);
+            if (qt + TQ > t.n) {  // query rows past the sequence
+                uint8_t* d = smem + kOffB + s * 2 * kSmall;
+                zero_rows(d, (t.n - qt) * G);
+                zero_rows(d + kSmall, (t.n - qt) * G);
+                fence_proxy_async_smem();
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.ready[0]);
+        }
+        if (ok && warp_wait(c.done, 0, c.abort_flag)) {
+            tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {  // dK, dV
+                float o[32];
+                tmem_ld32f((w ? tmV : tmK) + lane_off + half * 32, o);
+                tmem_ld_wait();
+                regs_ready<32>(o);
+                const float f = w ? 1.0f : a.scale;
+                const bool live = key < n_keys;
+                if (part) {
+                    float4* d = reinterpret_cast<float4*>(part + w * kD);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        d[u] = make_float4(o[4 * u] * f, o[4 * u + 1] * f, o[4 * u + 2] * f, o[4 * u + 3] * f);
+                } else if (dk) {
+                    T* d = w ? dv : dk;
+                    if (live) store_row32(d, o, f);
+                    else
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(d)[u] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    finish(c, warp, a.status);
+}
+
+template <typename K>
+lf_status opt_in(K kernel, std::atomic<bool>* done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LF_ERR_CUDA;
+    if (!done[dev].load()) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+            return LF_ERR_CUDA;
+        done[dev].store(true);
+    }
+    return LF_OK;
+}
+
+template <typename T>
+lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
+    static std::atomic<bool> attr[2][64];
+    lf_status st = opt_in(dq_kernel<T>, attr[0]);
+    if (st == LF_OK) st = opt_in(dkv_kernel<T>, attr[1]);
+    if (st != LF_OK) return st;
+    const int G = a.heads_group(), B = a.packed() ? 1 : a.n_seqs;
+    const lf_heads dout = {const_cast<void*>(a.dout), (long long)a.L * a.Hq * kD, kD, (long long)a.Hq * kD};
+    Maps mq, mk;
+    if (!make_heads_map(&mq.q, a.q, a.Hq, a.L, B, G, 128 / G) ||
+        !make_heads_map(&mq.dout, dout, a.Hq, a.L, B, G, 128 / G) ||
+        !make_heads_map(&mq.k, a.k, a.Hkv, a.L, B, 1, 64) || !make_heads_map(&mq.v, a.v, a.Hkv, a.L, B, 1, 64) ||
+        !make_heads_map(&mk.q, a.q, a.Hq, a.L, B, G, 64 / G) ||
+        !make_heads_map(&mk.dout, dout, a.Hq, a.L, B, G, 64 / G) ||
+        !make_heads_map(&mk.k, a.k, a.Hkv, a.L, B, 1, 128) || !make_heads_map(&mk.v, a.v, a.Hkv, a.L, B, 1, 128))
+        return LF_ERR_CUDA;
+    st = launch_pdl(dq_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, 128 / G), a.Hkv), dim3(kThreads),
+                    kSmemBytes, stream, mq, a);
+    if (st != LF_OK) return st;
+    const int slots = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.chunk) : 0;
+    const int items = slots * ((a.sinks + 127) / 128);
+    st = launch_pdl(dkv_kernel<T>, dim3(items + token_slots(a.packed(), a.n_seqs, a.L, 128), a.Hkv), dim3(kThreads),
+                    kSmemBytes, stream, mk, a, slots, items);
+    if (st == LF_OK && a.sinks > 0) st = launch_sink_reduce(a, stream);
+    return st;
+}
+
+}  // namespace
+
+lf_status launch_window_backward_tc(const WindowArgs& a, cudaStream_t stream) {
+    return a.dtype == LF_F16 ? backward_t<__half>(a, stream) : backward_t<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace lf

@@ -1,5 +1,5 @@
-// Windowed causal attention with sinks on the CUDA cores: forward (fp32) and
-// backward, fp32 arithmetic throughout.
+// Windowed causal attention with sinks in fp32 on the CUDA cores, forward and
+// backward (and the last step of every dtype's sink gradients).
 //
 //   forward   one CTA per tile of 64 query rows (64 / G tokens times the G
 //             query heads of a key/value head), online softmax over blocks
@@ -26,32 +26,16 @@ constexpr int kTile = kT * kLd;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
-template <>
-__device__ __forceinline__ float4 load4<__half>(const __half* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = Pair<__half>::unpack(u.x), b = Pair<__half>::unpack(u.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = Pair<__nv_bfloat16>::unpack(u.x), b = Pair<__nv_bfloat16>::unpack(u.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
 // 64 rows of 64 into a shared tile; row(r) is the row's address, NULL: zeros.
-template <typename T, typename F>
+template <typename F>
 __device__ __forceinline__ void load_tile(float* dst, F row) {
     const int c = (threadIdx.x & 15) * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (threadIdx.x >> 4) + 16 * i;
-        const T* p = row(r);
-        *reinterpret_cast<float4*>(dst + r * kLd + c) = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* p = row(r);
+        *reinterpret_cast<float4*>(dst + r * kLd + c) =
+            p ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -117,22 +101,14 @@ __device__ __forceinline__ float max16(float x) {
     return x;
 }
 
-template <typename T>
-__device__ __forceinline__ const T* view_row(const lf_heads& v, int batch, int head, int token) {
-    return static_cast<const T*>(v.data) + batch * v.batch_stride + head * v.head_stride + token * v.token_stride;
+__device__ __forceinline__ float* view_row(const lf_heads& v, int batch, int head, int token) {
+    return static_cast<float*>(v.data) + batch * v.batch_stride + head * v.head_stride + token * v.token_stride;
 }
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) p[c] = from_f<T>(x[c]);
-}
-template <>
-__device__ __forceinline__ void store4<float>(float* p, const float (&x)[4]) {
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 // ---------------------------------------------------------------- forward
-template <typename T>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ WindowArgs a) {
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kTile, *V = K + kTile, *P = V + kTile;
@@ -141,11 +117,11 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, blockIdx.x);
     if (t.t0 >= t.rows) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    auto q_row = [&](int r) -> const T* {
+    auto q_row = [&](int r) -> const float* {
         const int i = t.t0 + r / G;
-        return r < TQ * G && i < t.n ? view_row<T>(a.q, t.batch, hk * G + r % G, t.start + i) : nullptr;
+        return r < TQ * G && i < t.n ? view_row(a.q, t.batch, hk * G + r % G, t.start + i) : nullptr;
     };
-    load_tile<T>(Q, q_row);
+    load_tile(Q, q_row);
     float m[4], l[4], o[4][4];
     int pos[4];
 #pragma unroll
@@ -165,11 +141,11 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     for (int n = 0; n < kb.n; ++n) {
         const int c0 = key_block(kb, n) * kT;
         __syncthreads();
-        load_tile<T>(K, [&](int r) -> const T* {
-            return c0 + r < t.n ? view_row<T>(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
+        load_tile(K, [&](int r) -> const float* {
+            return c0 + r < t.n ? view_row(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
         });
-        load_tile<T>(V, [&](int r) -> const T* {
-            return c0 + r < t.n ? view_row<T>(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
+        load_tile(V, [&](int r) -> const float* {
+            return c0 + r < t.n ? view_row(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
         });
         __syncthreads();
         float s[4][4];
@@ -209,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][c] *= inv;
         const size_t row = (size_t)t.batch * a.L + t.start + tok;
-        store4(static_cast<T*>(a.out) + (row * a.Hq + h) * kD + 4 * tx, o[i]);
+        store4(static_cast<float*>(a.out) + (row * a.Hq + h) * kD + 4 * tx, o[i]);
         if (tx == 0)
             a.lse[((size_t)t.batch * a.Hq + h) * a.L + t.start + tok] =
                 l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
@@ -218,7 +194,6 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- dQ
 // Also leaves delta = rowsum(dO * out) for the kernels of dK and dV.
-template <typename T>
 __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ WindowArgs a) {
     extern __shared__ float sm[];
     float *Q = sm, *dO = Q + kTile, *K = dO + kTile, *V = K + kTile, *S = V + kTile;
@@ -231,11 +206,11 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ Wi
     auto o_off = [&](int r) {
         return (((size_t)t.batch * a.L + t.start + t.t0 + r / G) * a.Hq + hk * G + r % G) * kD;
     };
-    load_tile<T>(Q, [&](int r) -> const T* {
-        return live(r) ? view_row<T>(a.q, t.batch, hk * G + r % G, t.start + t.t0 + r / G) : nullptr;
+    load_tile(Q, [&](int r) -> const float* {
+        return live(r) ? view_row(a.q, t.batch, hk * G + r % G, t.start + t.t0 + r / G) : nullptr;
     });
-    load_tile<T>(dO, [&](int r) -> const T* { return live(r) ? static_cast<const T*>(a.dout) + o_off(r) : nullptr; });
-    load_tile<T>(K, [&](int r) -> const T* { return live(r) ? static_cast<const T*>(a.out) + o_off(r) : nullptr; });
+    load_tile(dO, [&](int r) -> const float* { return live(r) ? static_cast<const float*>(a.dout) + o_off(r) : nullptr; });
+    load_tile(K, [&](int r) -> const float* { return live(r) ? static_cast<const float*>(a.out) + o_off(r) : nullptr; });
     __syncthreads();
     float delta[4], lse[4], acc[4][4];
     int pos[4];
@@ -263,11 +238,11 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ Wi
     for (int n = 0; n < kb.n; ++n) {
         const int c0 = key_block(kb, n) * kT;
         __syncthreads();
-        load_tile<T>(K, [&](int r) -> const T* {
-            return c0 + r < t.n ? view_row<T>(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
+        load_tile(K, [&](int r) -> const float* {
+            return c0 + r < t.n ? view_row(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
         });
-        load_tile<T>(V, [&](int r) -> const T* {
-            return c0 + r < t.n ? view_row<T>(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
+        load_tile(V, [&](int r) -> const float* {
+            return c0 + r < t.n ? view_row(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
         });
         __syncthreads();
         float s[4][4], dp[4][4];
@@ -291,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ Wi
         if (r >= TQ * G || tok >= t.rows) continue;
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][c] *= a.scale;
-        store4(const_cast<T*>(view_row<T>(a.dq, t.batch, hk * G + r % G, t.start + tok)) + 4 * tx, acc[i]);
+        store4(view_row(a.dq, t.batch, hk * G + r % G, t.start + tok) + 4 * tx, acc[i]);
     }
 }
 
@@ -299,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ Wi
 // kSink false: one block of 64 keys over the queries that hold it in their
 // window.  kSink true: one block of sink keys over a chunk of the queries
 // that see it from outside their window; writes fp32 partial sums.
-template <typename T, bool kSink>
+template <bool kSink>
 __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ WindowArgs a) {
     extern __shared__ float sm[];
     float *K = sm, *V = K + kTile, *Q = V + kTile, *dO = Q + kTile, *P = dO + kTile, *S = P + kTile;
@@ -319,11 +294,11 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
         q0 = c0;
         q1 = (int)min((long long)t.n, (long long)c0 + kT + a.w);
     }
-    load_tile<T>(K, [&](int r) -> const T* {
-        return c0 + r < t.n ? view_row<T>(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
+    load_tile(K, [&](int r) -> const float* {
+        return c0 + r < t.n ? view_row(a.k, t.batch, hk, t.start + c0 + r) : nullptr;
     });
-    load_tile<T>(V, [&](int r) -> const T* {
-        return c0 + r < t.n ? view_row<T>(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
+    load_tile(V, [&](int r) -> const float* {
+        return c0 + r < t.n ? view_row(a.v, t.batch, hk, t.start + c0 + r) : nullptr;
     });
     float dk[4][4], dv[4][4];
 #pragma unroll
@@ -337,10 +312,10 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
             return (((size_t)t.batch * a.L + t.start + qt + r / G) * a.Hq + hk * G + r % G) * kD;
         };
         __syncthreads();
-        load_tile<T>(Q, [&](int r) -> const T* {
-            return live(r) ? view_row<T>(a.q, t.batch, hk * G + r % G, t.start + qt + r / G) : nullptr;
+        load_tile(Q, [&](int r) -> const float* {
+            return live(r) ? view_row(a.q, t.batch, hk * G + r % G, t.start + qt + r / G) : nullptr;
         });
-        load_tile<T>(dO, [&](int r) -> const T* { return live(r) ? static_cast<const T*>(a.dout) + o_off(r) : nullptr; });
+        load_tile(dO, [&](int r) -> const float* { return live(r) ? static_cast<const float*>(a.dout) + o_off(r) : nullptr; });
         if (threadIdx.x < kT) {
             const int r = threadIdx.x;
             const size_t at = ((size_t)t.batch * a.Hq + hk * G + r % G) * a.L + t.start + qt + r / G;
@@ -383,8 +358,8 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
             }
         }
         if (key >= t.rows) continue;
-        store4(const_cast<T*>(view_row<T>(a.dk, t.batch, hk, t.start + key)) + 4 * tx, dk[i]);
-        store4(const_cast<T*>(view_row<T>(a.dv, t.batch, hk, t.start + key)) + 4 * tx, dv[i]);
+        store4(view_row(a.dk, t.batch, hk, t.start + key) + 4 * tx, dk[i]);
+        store4(view_row(a.dv, t.batch, hk, t.start + key) + 4 * tx, dv[i]);
     }
 }
 
@@ -403,7 +378,8 @@ __global__ void __launch_bounds__(128) sink_reduce_kernel(const __grid_constant_
     const int chunks = (n + a.chunk - 1) / a.chunk;
     for (int c = 0; c < chunks; ++c) s += p[(size_t)(a.n_seqs + first + c) * step];
     const lf_heads& v = e < kD ? a.dk : a.dv;
-    const_cast<T*>(view_row<T>(v, a.cu ? 0 : b, hk, start + key))[e & (kD - 1)] = from_f<T>(s);
+    static_cast<T*>(v.data)[(a.cu ? 0 : b) * v.batch_stride + hk * v.head_stride + (start + key) * v.token_stride +
+                            (e & (kD - 1))] = from_f<T>(s);
 }
 
 template <typename K>
@@ -421,36 +397,24 @@ lf_status launch(K kernel, dim3 grid, int tiles, const A& a, cudaStream_t stream
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
-template <typename T>
-lf_status forward_t(const WindowArgs& a, cudaStream_t stream) {
+}  // namespace
+
+lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream) {
     const int TQ = kT / a.heads_group();
-    return launch(forward_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 4, a, stream);
+    return launch(forward_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 4, a, stream);
 }
 
-template <typename T>
-lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
+lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream) {
     const int TQ = kT / a.heads_group();
-    lf_status st = launch(dq_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 5, a, stream);
+    lf_status st = launch(dq_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 5, a, stream);
     if (st == LF_OK)
-        st = launch(dkv_kernel<T, false>, dim3(token_slots(a.packed(), a.n_seqs, a.L, kT), a.Hkv), 6, a, stream);
+        st = launch(dkv_kernel<false>, dim3(token_slots(a.packed(), a.n_seqs, a.L, kT), a.Hkv), 6, a, stream);
     if (st == LF_OK && a.sinks > 0) {
-        st = launch(dkv_kernel<T, true>,
+        st = launch(dkv_kernel<true>,
                     dim3(token_slots(a.packed(), a.n_seqs, a.L, a.chunk), a.Hkv, (a.sinks + kT - 1) / kT), 6, a, stream);
         if (st == LF_OK) st = launch_sink_reduce(a, stream);
     }
     return st;
-}
-
-}  // namespace
-
-lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream) {
-    return forward_t<float>(a, stream);
-}
-
-lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream) {
-    if (a.dtype == LF_F16) return backward_t<__half>(a, stream);
-    if (a.dtype == LF_BF16) return backward_t<__nv_bfloat16>(a, stream);
-    return backward_t<float>(a, stream);
 }
 
 lf_status launch_sink_reduce(const WindowArgs& a, cudaStream_t stream) {
