@@ -546,8 +546,8 @@ size_t lf_paged_attention_workspace_bytes(int n_seqs, int Hq, int Hkv, int T, in
  * LF_ERR_BAD_LENGTHS), gets zeros.  kv_lens[b] beyond the table's width is
  * clamped and recorded as LF_ERR_BAD_LENGTHS.
  * Errors: LF_ERR_NULL, LF_ERR_BAD_DIM, LF_ERR_DTYPE, LF_ERR_MISALIGNED,
- * LF_ERR_TOO_LARGE (T * Hq >= 2^31, max_pages * page_size >= 2^30, n_seqs >=
- * 2^23, Hkv > 65535), LF_ERR_WORKSPACE.  T = 0 does nothing.  Asynchronous.
+ * LF_ERR_TOO_LARGE (T * Hq >= 2^31, max_pages * page_size > 2^24, n_seqs >=
+ * 2^21, Hkv > 65535), LF_ERR_WORKSPACE.  T = 0 does nothing.  Asynchronous.
  */
 lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache, const lf_heads* v_cache,
                                      const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* kv_lens,

@@ -1,0 +1,71 @@
+// How a paged attention call is cut into CTAs: which of the two kernels it
+// needs and into how many pieces each cuts a context.  Host arithmetic on
+// the bounds a caller gives (lengths live on the device), and the geometry
+// both kernels and the merge agree on.
+#pragma once
+
+#include "lf_visible.h"
+
+namespace lf {
+
+// Sequences with at most this many query rows per key/value head (new tokens
+// x grouped heads) go to the decode kernel, one mma.m16n8k16 tile of rows.
+constexpr int kDecodeRows = 16;
+
+struct PagedPlan {
+    bool decode, tensor;  // kernels launched
+    int chunk;            // decode: tiles of 8 keys per CTA
+    int decode_splits;    // pieces of a context (n_seqs times that: its gridDim.x)
+    int per;              // tensor cores: blocks of 64 keys per CTA
+    int tensor_splits;    // its gridDim.z
+    float* o;             // [splits][T * Hq][64]
+    float* lse;           // [splits][T * Hq], log2
+    LF_HD int splits() const { return imax(decode ? decode_splits : 1, tensor ? tensor_splits : 1); }
+};
+
+// The tiles of 8 keys a sequence's n new tokens from position `first` see.
+LF_HD KeyBlocks decode_tiles(int first, int n, int kv, int w, int sinks) {
+    KeyBlocks k = {0, 0, 0};
+    return first + n - 1 >= 0 ? key_blocks(first, first + n - 1, kv, w, sinks, 8) : k;
+}
+// The blocks of 64 keys that the tokens [t0, t1) see.
+LF_HD KeyBlocks tile_key_blocks(int first, int t0, int t1, int kv, int w, int sinks) {
+    KeyBlocks k = {0, 0, 0};
+    return t0 < t1 && first + t1 - 1 >= 0 ? key_blocks(first + t0, first + t1 - 1, kv, w, sinks, 64) : k;
+}
+
+// w and sinks clamped to the table's width.
+inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int width, int w, int sinks) {
+    PagedPlan p = {};
+    const int G = Hq / Hkv;
+    p.tensor = (long long)max_q * G > kDecodeRows;
+    // (with n_seqs * max_q tokens every sequence has max_q)
+    p.decode = G <= kDecodeRows && !(p.tensor && (long long)n_seqs * max_q == T);
+    // Keys one sequence's tokens can see, at most.
+    const long long seen = width < (long long)w + max_q + sinks ? width : (long long)w + max_q + sinks;
+    if (p.decode) {
+        // About two rounds of CTAs (three of 4 warps fit an SM) over the
+        // widest contexts, 128 to 1024 keys each: fewer, and a warp has no
+        // second step to load under its first; more, and ragged contexts
+        // leave SMs idle.
+        const long long tiles = seen / 8 + 2, all = tiles * n_seqs * Hkv;
+        p.chunk = (int)(all / (2 * 3 * 148));
+        p.chunk = iclamp((p.chunk + 15) / 16 * 16, 16, 128);
+        if (tiles > 1024LL * p.chunk) p.chunk = (int)((tiles + 1023) / 1024);  // at most 1024 pieces
+        p.decode_splits = (int)((tiles + p.chunk - 1) / p.chunk);
+    }
+    if (p.tensor) {
+        // Split only when the tiles leave most of the 4 x 148 CTA slots idle,
+        // into pieces of at least 8 blocks.
+        const long long tiles = (long long)packed_slots(T, n_seqs, 128 / G) * Hkv;
+        const long long blocks = seen / 64 + 2;
+        const long long want = (4 * 148) / tiles;
+        long long per = want > 1 ? (blocks + want - 1) / want : blocks;
+        if (per < 8) per = 8;
+        p.per = (int)per;
+        p.tensor_splits = (int)((blocks + per - 1) / per);
+    }
+    return p;
+}
+
+}  // namespace lf

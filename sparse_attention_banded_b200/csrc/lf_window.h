@@ -3,6 +3,7 @@
 #pragma once
 
 #include "lf_internal.h"
+#include "lf_paged_split.h"
 #include "lf_visible.h"
 
 namespace lf {
@@ -62,7 +63,6 @@ struct PagedArgs {
     lf_dtype dtype;
     void* out;                // [T][Hq * 64]
     int* status;
-    void* workspace;
     int heads_group() const { return Hq / Hkv; }
 };
 // Where sequence b's n new tokens stand: kv keys in all (clamped to the
@@ -86,7 +86,8 @@ __device__ __forceinline__ void check_lengths(const int32_t* cu, const int32_t* 
     }
 }
 lf_status launch_paged_append(const PagedArgs& a, cudaStream_t stream);
-lf_status launch_paged_forward_tc(const PagedArgs& a, cudaStream_t stream);
+lf_status launch_paged_forward(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
+lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& plan, cudaStream_t stream);
 
 // ---- layer norm ----
 struct NormArgs {

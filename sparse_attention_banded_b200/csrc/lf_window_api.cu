@@ -75,7 +75,7 @@ lf_status check_paged_sizes(int n_seqs, int Hq, int Hkv, int T, int max_pages, i
     if (n_seqs <= 0 || Hq <= 0 || Hkv <= 0 || T < 0 || max_pages <= 0 || num_pages <= 0) return LF_ERR_BAD_DIM;
     if (page_size < 8 || page_size > 4096 || (page_size & (page_size - 1))) return LF_ERR_BAD_DIM;
     if (Hq % Hkv != 0 || Hq / Hkv > 64) return LF_ERR_BAD_DIM;
-    if ((T > 0 && Hq > (kInt31 - 1) / T) || (long long)max_pages * page_size >= kMostPositions || n_seqs >= (1 << 23) ||
+    if ((T > 0 && Hq > (kInt31 - 1) / T) || (long long)max_pages * page_size > (1LL << 24) || n_seqs >= (1 << 21) ||
         Hkv > 65535)
         return LF_ERR_TOO_LARGE;
     return LF_OK;
@@ -208,8 +208,15 @@ lf_status lf_paged_cache_append(const lf_heads* k_new, const lf_heads* v_new, co
 
 size_t lf_paged_attention_workspace_bytes(int n_seqs, int Hq, int Hkv, int T, int max_q_len, int max_pages,
                                           int page_size, int w, int sinks) {
-    (void)n_seqs; (void)Hq; (void)Hkv; (void)T; (void)max_q_len; (void)max_pages; (void)page_size; (void)w; (void)sinks;
-    return 0;
+    if (check_paged_sizes(n_seqs, Hq, Hkv, T, max_pages, 1, page_size) != LF_OK || T == 0 || max_q_len <= 0 || w < 0 ||
+        sinks < 0)
+        return 0;
+    const int width = max_pages * page_size;
+    const PagedPlan p =
+        paged_plan(n_seqs, Hq, Hkv, T, imin(max_q_len, T), width, imin(w, width), imin(sinks, width));
+    if (p.splits() <= 1) return 0;
+    const size_t rows = (size_t)p.splits() * T * Hq;
+    return align256(rows * 64 * sizeof(float)) + align256(rows * sizeof(float));
 }
 
 lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache, const lf_heads* v_cache,
@@ -253,8 +260,10 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
     a.dtype = dtype;
     a.out = out;
     a.status = d->status;
-    a.workspace = workspace;
-    return launch_paged_forward_tc(a, (cudaStream_t)stream);
+    PagedPlan plan = paged_plan(n_seqs, Hq, Hkv, T, a.max_q, max_pages * page_size, a.w, a.sinks);
+    plan.o = static_cast<float*>(workspace);
+    plan.lse = plan.o + align256((size_t)plan.splits() * T * Hq * 64 * sizeof(float)) / sizeof(float);
+    return launch_paged_forward(a, plan, (cudaStream_t)stream);
 }
 
 lf_status lf_layer_norm_forward(const void* x, long long x_stride, const float* gamma, const float* beta, int rows,

@@ -19,7 +19,7 @@
 // Paged: a block is gathered by one TMA box per page (of up to 64
 // positions).  Long contexts of few tiles are split over gridDim.z CTAs of
 // `per` blocks each, which leave normalised fp32 rows and their log2-sum-exp
-// for a merge kernel.
+// for the merge kernel.
 #include <atomic>
 #include <mutex>
 
@@ -85,17 +85,9 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-struct Split {
-    int per;      // key blocks per split
-    int splits;   // gridDim.z
-    int min_rows; // paged: tiles of sequences with fewer rows belong to the decode kernel
-    float* o;     // [splits][T * Hq][64]
-    float* lse;   // [splits][T * Hq], log2
-};
-
 template <typename T, bool kPaged, typename A>
 __global__ void __launch_bounds__(kThreads, kCtas)
-window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, const __grid_constant__ Split sp) {
+window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, const __grid_constant__ PagedPlan pl) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
@@ -124,16 +116,18 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     if (t.t0 >= t.rows) return;
     int first = 0, n_keys = t.n;  // position of the first token, keys in all
     if constexpr (kPaged) {
-        if (t.n * G < sp.min_rows) return;
+        if (pl.decode && t.n * G <= kDecodeRows) return;  // the decode kernel's
         if (!paged_seq(a, t.b, t.n, n_keys, first, threadIdx.x == 0 && hk == 0 && blockIdx.z == 0 && t.t0 == 0)) return;
     }
     const int i0 = first + t.t0, i1 = first + imin(t.t0 + TQ, t.n) - 1;  // positions of the tile's tokens
-    KeyBlocks kb = {0, 0, 0};
-    if (t.t0 < t.n && i1 >= 0) kb = key_blocks(i0, i1, n_keys, a.w, a.sinks, kBN);
+    const KeyBlocks kb = tile_key_blocks(first, t.t0, imin(t.t0 + TQ, t.n), n_keys, a.w, a.sinks);
     int b0 = 0, b1 = kb.n;
+    bool part = false;  // one piece of several
     if constexpr (kPaged) {
-        b0 = imin(blockIdx.z * sp.per, kb.n);
-        b1 = imin(b0 + sp.per, kb.n);
+        b0 = imin(blockIdx.z * pl.per, kb.n);
+        b1 = imin(b0 + pl.per, kb.n);
+        part = kb.n > pl.per;
+        if (b0 == b1 && blockIdx.z > 0) return;
     }
     const int nb = b1 - b0;
 
@@ -144,12 +138,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
 
     if (nb == 0) {  // padding, or nothing to see: zeros
         if (r >= kBM || !row_stored) return;
-        if constexpr (kPaged) {
-            if (sp.splits > 1) {
-                sp.lse[(size_t)blockIdx.z * ((size_t)a.T * a.Hq) + orow] = -INFINITY;
-                return;
-            }
-        } else {
+        if constexpr (!kPaged) {
             a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = -INFINITY;
         }
         zero_row64(static_cast<T*>(a.out) + orow * kD);
@@ -213,7 +202,9 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     unsigned long long m = 0;
                     for (int u = 0; u < boxes; ++u)
                         if ((have >> u) & 1) m |= low_bits64(rows) << (u * rows);
-                    valid[s] = m & low_bits64(n_keys - c0);
+                    // and only keys some row sees: others' values may be anything
+                    valid[s] = m & low_bits64(imin(n_keys, i1 + 1) - c0) &
+                               (~low_bits64(imax(i0, 0) - a.w - c0) | low_bits64(a.sinks - c0));
                     const uint32_t bytes = __popc(have) * rows * kD * 2;
                     if (bytes) {
                         mbar_arrive_expect_tx(&k_full[s], bytes);
@@ -403,8 +394,6 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             if (i < 0) l = 0.0f;  // no token of the sequence
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-            bool part = false;
-            if constexpr (kPaged) part = sp.splits > 1;
             const size_t at = part ? (size_t)blockIdx.z * ((size_t)L * a.Hq) + orow : 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -417,7 +406,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     for (int c = 0; c < 32; ++c) o[c] = 0.0f;
                 }
                 if (row_stored && part) {
-                    float4* d = reinterpret_cast<float4*>(sp.o + at * kD + h * 32);
+                    float4* d = reinterpret_cast<float4*>(pl.o + at * kD + h * 32);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         d[c] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
@@ -427,7 +416,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 __syncwarp();
             }
             if (row_stored) {
-                if (part) sp.lse[at] = lse2;
+                if (part) pl.lse[at] = lse2;
                 if constexpr (!kPaged) a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = lse2 * kLn2;
             }
         }
@@ -442,7 +431,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
 }
 
 template <typename T, bool kPaged, typename A>
-lf_status launch(const Maps& maps, const A& a, const Split& sp, dim3 grid, cudaStream_t stream) {
+lf_status launch(const Maps& maps, const A& a, const PagedPlan& pl, dim3 grid, cudaStream_t stream) {
     static std::atomic<bool> attr[64];  // the shared-memory opt-in, per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LF_ERR_CUDA;
@@ -452,7 +441,7 @@ lf_status launch(const Maps& maps, const A& a, const Split& sp, dim3 grid, cudaS
             return LF_ERR_CUDA;
         attr[dev].store(true);
     }
-    return launch_pdl(window_kernel<T, kPaged, A>, grid, dim3(kThreads), kSmemBytes, stream, maps, a, sp);
+    return launch_pdl(window_kernel<T, kPaged, A>, grid, dim3(kThreads), kSmemBytes, stream, maps, a, pl);
 }
 
 }  // namespace
@@ -464,22 +453,21 @@ lf_status launch_window_forward_tc(const WindowArgs& a, cudaStream_t stream) {
         !make_heads_map(&maps.v, a.v, a.Hkv, a.L, B, 1, kBN))
         return LF_ERR_CUDA;
     const dim3 grid(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv);
-    const Split sp = {0, 1, 0, nullptr, nullptr};
-    if (a.dtype == LF_F16) return launch<__half, false>(maps, a, sp, grid, stream);
-    return launch<__nv_bfloat16, false>(maps, a, sp, grid, stream);
+    const PagedPlan pl = {};
+    if (a.dtype == LF_F16) return launch<__half, false>(maps, a, pl, grid, stream);
+    return launch<__nv_bfloat16, false>(maps, a, pl, grid, stream);
 }
 
-lf_status launch_paged_forward_tc(const PagedArgs& a, cudaStream_t stream) {
+lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& pl, cudaStream_t stream) {
     const int G = a.heads_group(), TQ = kBM / G, page = 1 << a.page_shift;
     Maps maps;
     if (!make_heads_map(&maps.q, a.q, a.Hq, a.T, 1, G, TQ) ||
         !make_heads_map(&maps.k, a.k, a.Hkv, page, a.num_pages, 1, imin(page, kBN)) ||
         !make_heads_map(&maps.v, a.v, a.Hkv, page, a.num_pages, 1, imin(page, kBN)))
         return LF_ERR_CUDA;
-    const dim3 grid(packed_slots(a.T, a.n_seqs, TQ), a.Hkv);
-    const Split sp = {INT32_MAX / 2, 1, 0, nullptr, nullptr};
-    if (a.dtype == LF_F16) return launch<__half, true>(maps, a, sp, grid, stream);
-    return launch<__nv_bfloat16, true>(maps, a, sp, grid, stream);
+    const dim3 grid(packed_slots(a.T, a.n_seqs, TQ), a.Hkv, pl.tensor_splits);
+    if (a.dtype == LF_F16) return launch<__half, true>(maps, a, pl, grid, stream);
+    return launch<__nv_bfloat16, true>(maps, a, pl, grid, stream);
 }
 
 }  // namespace lf

@@ -34,7 +34,7 @@ class Case:
     is NaN, and so are the pages of no sequence."""
 
     def __init__(self, qlens, kvlens, Hq, Hkv, page, dtype="f16", seed=0, w=ALL, sinks=0, token_major=False, tail=2,
-                 free=True, extra=3):
+                 free=True, extra=3, stale=False):
         g = torch.Generator().manual_seed(seed)
         r = random.Random(seed)
         dt = DT[dtype]
@@ -57,6 +57,8 @@ class Case:
                 p = pool.pop()
                 lo, hi = j * page, min(kvlens[b], (j + 1) * page)
                 if free and hi <= first and lo >= sinks:
+                    if stale:
+                        table[b, j] = p  # the entry still names a page, which holds NaN
                     continue  # wholly behind the window: freed
                 table[b, j] = p
                 old = kvlens[b] - qlens[b]  # the new tokens' slots are filled by the append
@@ -117,6 +119,20 @@ def test_grouped_heads(Hq, Hkv, qlen):
 @pytest.mark.parametrize("qlens", [[1, 1, 1, 1], [70, 1, 3, 200]])
 def test_windows_sinks_and_freed_pages(w, sinks, qlens):
     Case(qlens, [70, 400, 1111, 2500], 4, 1, 16, "bf16", seed=w % 97 + sinks, w=w, sinks=sinks).run().check()
+
+
+@pytest.mark.parametrize("page", [8, 64])
+def test_what_no_query_sees_may_be_anything(page):
+    """Stale table entries behind the window, and the positions before the
+    window (or past the sinks) in pages that are still held: NaN."""
+    c = Case([1, 70, 3, 2], [700, 400, 1111, 90], 4, 2, page, "bf16", seed=page, w=100, sinks=3, stale=True)
+    for b, (n, m) in enumerate(zip(c.qlens, c.kvlens)):
+        for j in range(c.sinks, max(c.sinks, m - n - c.w)):
+            p = int(c.table[b, j // page])
+            if p >= 0:
+                c.kc[p, :, j % page] = float("nan")
+                c.vc[p, :, j % page] = float("nan")
+    c.run().check()
 
 
 def test_cache_with_heads_inside_pages():

@@ -93,7 +93,7 @@ def _paged(L, q=None, kc=None, vc=None, table=FAKE, cu=FAKE, kv=FAKE, n=2, Hq=4,
     (dict(scale=0.0), 2), (dict(q=_h(st=0)), 2), (dict(kc=_h(sb=-64)), 2),
     (dict(dtype=0), 7), (dict(dtype=9), 7),
     (dict(kc=_h(st=68)), 8), (dict(out=FAKE + 8), 8), (dict(table=FAKE + 2), 8),
-    (dict(T=1 << 30), 13), (dict(mp=1 << 27), 13), (dict(n=1 << 23), 13),
+    (dict(T=1 << 30), 13), (dict(mp=(1 << 20) + 1), 13), (dict(n=1 << 21), 13),
 ])
 def test_paged_forward_refusals(L, kw, status):
     assert _paged(L, **kw) == status
