@@ -133,6 +133,21 @@ LF_HD unsigned long long visible_bits(int i, int c0, int n_keys, int w, int sink
     return causal & (~low_bits64(i - w - c0) | low_bits64(sinks - c0));
 }
 
+// Bits [0, n) of a 32-bit word, n clamped to [0, 32].
+LF_HD unsigned low_bits32(int n) {
+#ifdef __CUDA_ARCH__
+    unsigned m;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(imax(n, 0)));
+    return m;
+#else
+    return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+#endif
+}
+// The same as visible_bits for the 32 keys from c0 on.
+LF_HD unsigned visible_bits32(int i, int c0, int n_keys, int w, int sinks) {
+    return low_bits32(imin(i + 1, n_keys) - c0) & (~low_bits32(i - w - c0) | low_bits32(sinks - c0));
+}
+
 // ---- paged cache ----------------------------------------------------------
 // The page of key position j in a sequence's table row, -1 where the table
 // has none: past its width, or an entry outside [0, num_pages).

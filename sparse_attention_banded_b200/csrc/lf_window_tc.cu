@@ -5,15 +5,21 @@
 // that share a key/value head, so grouped heads read each key block once and
 // a tile's keys span only w + 128 / G positions.  Per block of 64 keys:
 //     S = Q K^T                        (tcgen05.mma, fp32 in tensor memory)
-//     m' = max(m, max s), P = 2^(s - m'), l += sum P        (one thread a row)
+//     m' = max(m, max s), P = 2^(s - m'), l += sum P
 //     O = O 2^(m - m') + P V           (P from tensor memory)
-// S and O take 64 tensor-memory columns each, P the columns of its S, so four
-// CTAs share an SM: a CTA's steps are a chain of latencies (product, softmax,
-// product), and the four chains fill each other's gaps.  The O update is
-// skipped unless a row's maximum grows by more than 2^8 (P <= 2^8 then).
-// P is rounded to the storage type, the MMA's operand type; sums stay fp32.
+// Two threads share a row, each with its own half of every block's keys, its
+// own m, l and O: they meet only at the tile's end, as two pieces of a split
+// context would.  S has two buffers, so the next block's S runs under this
+// one's softmax and the softmax warps never wait for a product; P overwrites
+// the first 16 columns of its half of S.  S, S and two O's take 256 tensor-
+// memory columns: two CTAs per SM.  (One thread a row, one S buffer and four
+// CTAs per SM left every CTA a chain of latencies: 195 us at 16384 packed
+// tokens, 16 / 4 heads, window 1024, 37 % of the issue slots used.)
+// The O update is skipped unless a row's maximum grows by more than 2^8 (P
+// <= 2^8 then).  P is rounded to the storage type, the MMA's operand type;
+// sums stay fp32.
 //
-// Warps 0-3: softmax and epilogue, warp 4: TMA loads, warp 5: MMAs.  All
+// Warps 0-7: softmax and epilogue, warp 8: TMA loads, warp 9: MMAs.  All
 // waits are bounded (LF_ERR_DEVICE_TIMEOUT).
 //
 // Paged: a block is gathered by one TMA box per page (of up to 64
@@ -67,19 +73,21 @@ using namespace sm100;
 constexpr int kBM = 128;   // query rows
 constexpr int kBN = 64;    // keys per block
 constexpr int kD = 64;
-constexpr int kStages = 2;
-constexpr int kThreads = 192;
-constexpr int kCtas = 4;   // per SM
+constexpr int kStages = 3;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kCtas = 2;   // per SM
 constexpr uint32_t kQBytes = kBM * kD * 2, kKBytes = kBN * kD * 2;
-constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffBar = kOffV + kStages * kKBytes;
-constexpr uint32_t kBars = 1 + 3 * kStages + 4;
+constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffMl = kOffV + kStages * kKBytes;
+constexpr uint32_t kOffBar = kOffMl + 2 * kBM * 8;               // (m, l) of both halves
+constexpr uint32_t kBars = 1 + 3 * kStages + 7;
 constexpr uint32_t kOffMask = kOffBar + kBars * 8;               // valid keys of each stage (paged)
 constexpr uint32_t kOffMisc = kOffMask + kStages * 8;
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;            // + alignment slack
-constexpr uint32_t kTmemCols = 128, kTmemO = 64;
+constexpr uint32_t kTmemCols = 256, kTmemO = 128;                // S at 0 and 64, O at 128 and 192
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
-static_assert(kCtas * (kSmemBytes + 1024) <= 227 * 1024 + 1024, "four CTAs per SM");
+static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -95,9 +103,11 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     uint64_t* v_full = k_full + kStages;
     uint64_t* kv_empty = v_full + kStages;
     uint64_t* s_full = kv_empty + kStages;
-    uint64_t* p_full = s_full + 1;
-    uint64_t* o_full = p_full + 1;
+    uint64_t* p_full = s_full + 2;  // (both [2]: per S buffer)
+    uint64_t* pv_done = p_full + 2;
+    uint64_t* o_full = pv_done + 1;
     uint64_t* drain = o_full + 1;
+    float2* ml = reinterpret_cast<float2*>(smem + kOffMl);
     volatile unsigned long long* valid = reinterpret_cast<volatile unsigned long long*>(smem + kOffMask);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
@@ -131,13 +141,13 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     }
     const int nb = b1 - b0;
 
-    // this thread's row (softmax warps)
-    const int r = threadIdx.x, tok = t.t0 + r / G, head = hk * G + r % G;
+    // this thread's row and half (softmax warps)
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2, tok = t.t0 + r / G, head = hk * G + r % G;
     const bool row_stored = r < TQ * G && tok < t.rows;
     const size_t orow = ((size_t)t.batch * L + t.start + tok) * a.Hq + head;
 
     if (nb == 0) {  // padding, or nothing to see: zeros
-        if (r >= kBM || !row_stored) return;
+        if (half > 0 || !row_stored) return;
         if constexpr (!kPaged) {
             a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = -INFINITY;
         }
@@ -152,18 +162,21 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             mbar_init(&v_full[s], 1);
             mbar_init(&kv_empty[s], 1);
         }
-        mbar_init(s_full, 1);
-        mbar_init(p_full, 4);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(&p_full[0], kSoftmaxWarps);
+        mbar_init(&p_full[1], kSoftmaxWarps);
+        mbar_init(pv_done, 1);
         mbar_init(o_full, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 5) {
+    if (warp == kSoftmaxWarps + 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == kSoftmaxWarps && lane == 0) {
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);
@@ -173,7 +186,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 4) {
+    if (warp == kSoftmaxWarps) {
         // ------------------------------------------------------------ TMA
         bool ok = true;
         if (lane == 0) {
@@ -236,37 +249,43 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 mbar_wait(&v_full[c % kStages], (c / kStages) & 1, &never, 200000000ull);
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == kSoftmaxWarps + 1) {
         // ------------------------------------------------------------ MMA
-        // In issue order S_0, PV_0, S_1, PV_1, ...: the products run in that
-        // order, so S_j may overwrite P_(j-1) without waiting for PV_(j-1).
+        // In issue order S_0, S_1, PV_0, S_2, PV_1, ...: the products run in
+        // that order, so S_(j+1) may overwrite P_(j-1) without a wait.
         constexpr uint32_t id_s = idesc_f16(MmaFormat<T>::fmt, kBM, kBN, 0, 0);
         constexpr uint32_t id_o = idesc_f16(MmaFormat<T>::fmt, kBM, kD, 0, 1);
         const uint64_t dq = desc_sw128(smem_u32(smem)), dk = desc_sw128(smem_u32(smem + kOffK)),
                        dv = desc_sw128(smem_u32(smem + kOffV), 0);
-        bool ok = warp_wait(q_full, 0, abort_flag);
-        for (int j = 0; j < nb && ok; ++j) {
+        auto scores = [&](int j) -> bool {
             const int s = j % kStages;
-            const uint32_t par = (j / kStages) & 1;
-            ok = warp_wait(&k_full[s], par, abort_flag);
-            if (!ok) break;
+            if (!warp_wait(&k_full[s], (j / kStages) & 1, abort_flag)) return false;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
                 for (int kk = 0; kk < kD / 16; ++kk)
-                    mma_f16_ss(tmem, dq + kk * 2, dk + s * (kKBytes >> 4) + kk * 2, id_s, kk > 0);
-                tc_commit(s_full);
+                    mma_f16_ss(tmem + (j & 1) * kBN, dq + kk * 2, dk + s * (kKBytes >> 4) + kk * 2, id_s, kk > 0);
+                tc_commit(&s_full[j & 1]);
             }
             __syncwarp();
-            ok = warp_wait(&v_full[s], par, abort_flag) && warp_wait(p_full, j & 1, abort_flag);
+            return true;
+        };
+        bool ok = warp_wait(q_full, 0, abort_flag) && scores(0);
+        for (int j = 0; j < nb && ok; ++j) {
+            const int s = j % kStages;
+            // S_(j+1) reuses the buffer of P_(j-1): its PV has been issued
+            if (j + 1 < nb) ok = scores(j + 1);
+            ok = ok && warp_wait(&v_full[s], (j / kStages) & 1, abort_flag) &&
+                 warp_wait(&p_full[j & 1], (j >> 1) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)
-                    mma_f16_ts(tmem + kTmemO, tmem + kk * 8, dv + s * (kKBytes >> 4) + kk * (2048 >> 4), id_o,
-                               j > 0 || kk > 0);
+                for (int kk = 0; kk < kBN / 16; ++kk)  // two steps of 16 keys for each half's O
+                    mma_f16_ts(tmem + kTmemO + (kk >> 1) * kD, tmem + (j & 1) * kBN + (kk >> 1) * 32 + (kk & 1) * 8,
+                               dv + s * (kKBytes >> 4) + kk * (2048 >> 4), id_o, j > 0 || (kk & 1));
                 tc_commit(&kv_empty[s]);
+                tc_commit(pv_done);
                 if (j == nb - 1) tc_commit(o_full);
             }
             __syncwarp();
@@ -278,153 +297,144 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
         }
     } else {
         // ------------------------------------------------------------ softmax
-        const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16), tO = tS + kTmemO;
+        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tO = t_lane + kTmemO + half * kD;
         const int i = r < TQ * G && tok < t.n ? first + tok : -1;
         const float sc = a.scale * kLog2e;
+        // blocks that every row sees whole begin in [full_lo, full_hi]
+        const int full_lo = i1 - a.w, full_hi = imin(i0 + 1, n_keys) - kBN;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < nb; ++j) {
             const int s = j % kStages, c0 = key_block(kb, b0 + j) * kBN;
-            ok = warp_wait(s_full, j & 1, abort_flag);
+            const uint32_t tS = t_lane + (j & 1) * kBN + half * 32;
+            bool full = c0 <= full_hi && c0 >= full_lo;
+            ok = warp_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            unsigned long long have = low_bits64(n_keys - c0);
+            float x[32];
+            tmem_ld32f(tS, x);
+            unsigned long long have = ~0ull;  // keys that exist (and, paged, that some row sees)
             if constexpr (kPaged) {
                 // (published before the loads of the stage were issued)
                 ok = warp_wait(&k_full[s], (j / kStages) & 1, abort_flag);
                 if (!ok) break;
                 have = valid[s];
+                full = full && have == ~0ull;
+            } else if (c0 + kBN > n_keys) {
+                have = low_bits64(n_keys - c0);
             }
-            const bool full = have == ~0ull && block_full(i0, i1, c0, kBN, n_keys, a.w, a.sinks);
-            uint32_t bits[2] = {~0u, ~0u};
+            tmem_ld_wait();
+            regs_ready<32>(x);
             if (!full) {
-                const unsigned long long vis = i >= 0 ? visible_bits(i, c0, n_keys, a.w, a.sinks) & have : 0ull;
-                bits[0] = (uint32_t)vis;
-                bits[1] = (uint32_t)(vis >> 32);
-            }
-            // Two passes over S in halves of 32 columns (32 live scores: four
-            // CTAs of 192 threads leave 80 registers a thread): the maximum,
-            // then the exponentials.
-            auto scores = [&](int h, float (&x)[32]) {
-                tmem_ld32f(tS + h * 32, x);
-                tmem_ld_wait();
-                regs_ready<32>(x);
-                if (!full) {
+                const uint32_t bits = visible_bits32(i, c0 + half * 32, n_keys, a.w, a.sinks) & (uint32_t)(have >> (32 * half));
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] = (bits[h] >> c) & 1 ? x[c] : -INFINITY;
-                }
-            };
+                for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1 ? x[c] : -INFINITY;
+            }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                scores(h, x);
-#pragma unroll
-                for (int c = 0; c < 32; c += 8) {
-                    mx[0] = max3(mx[0], x[c], x[c + 1]);
-                    mx[1] = max3(mx[1], x[c + 2], x[c + 3]);
-                    mx[2] = max3(mx[2], x[c + 4], x[c + 5]);
-                    mx[3] = max3(mx[3], x[c + 6], x[c + 7]);
-                }
+            for (int c = 0; c < 32; c += 8) {
+                mx[0] = max3(mx[0], x[c], x[c + 1]);
+                mx[1] = max3(mx[1], x[c + 2], x[c + 3]);
+                mx[2] = max3(mx[2], x[c + 4], x[c + 5]);
+                mx[3] = max3(mx[3], x[c + 6], x[c + 7]);
             }
             const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
             const bool need = cm > m + kRescale || (m == -INFINITY && cm > m);
             if (__any_sync(0xffffffffu, need)) {
                 const bool real = need && m != -INFINITY;
                 if (__any_sync(0xffffffffu, real)) {
-                    // (S_j is complete, and with it every earlier product:
-                    // O is not being written)
+                    // every earlier product into O must be done (PV_(j-2) and
+                    // before are, since S_j is)
+                    ok = warp_wait(pv_done, (j - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
                     const float f = real ? ex2(m - cm) : 1.0f;
                     l *= f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float o[32];
-                        tmem_ld32f(tO + h * 32, o);
+                    for (int h = 0; h < 4; ++h) {
+                        float o[16];
+                        tmem_ld16f(tO + h * 16, o);
                         tmem_ld_wait();
-                        regs_ready<32>(o);
+                        regs_ready<16>(o);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] *= f;
-                        tmem_st32f(tO + h * 32, o);
+                        for (int c = 0; c < 16; ++c) o[c] *= f;
+                        tmem_st16f(tO + h * 16, o);
                     }
                 }
                 if (need) m = cm;
             }
             const float nm = m == -INFINITY ? 0.0f : -m;
-            const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t pk[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                uint32_t pk[16];
-                scores(h, x);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const float2 v = ffma2(make_float2(x[2 * c], x[2 * c + 1]), sc2, nm2);
-                    float2 e;
-                    // a third of a full block's exponentials on the FMA pipe;
-                    // masked scores (-inf) need the exact 0 of the other path
-                    if (c % 3 == 2 && full) e = exp2_poly2(v);
-                    else e = make_float2(ex2(v.x), ex2(v.y));
-                    sum[c & 1] = fadd2(sum[c & 1], e);
-                    pk[c] = Pair<T>::pack(e.x, e.y);
-                }
-                tmem_st16(tS + h * 16, pk);
+            for (int c = 0; c < 16; ++c) {
+                const float e0 = ex2(fmaf(x[2 * c], sc, nm)), e1 = ex2(fmaf(x[2 * c + 1], sc, nm));
+                sum[(2 * c) & 3] += e0;
+                sum[(2 * c + 1) & 3] += e1;
+                pk[c] = Pair<T>::pack(e0, e1);
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st16(tS, pk);
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (have != ~0ull) {
                 // rows of V that are no key of the sequence: 0 * NaN is NaN
                 ok = warp_wait(&v_full[s], (j / kStages) & 1, abort_flag);
                 if (!ok) break;
-                const int row = threadIdx.x >> 1;
+                const int row = threadIdx.x >> 2;
                 if (!((have >> row) & 1)) {
-                    uint4* z = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 1) * 64);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) z[c] = make_uint4(0u, 0u, 0u, 0u);
+                    uint4* z = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 3) * 32);
+                    z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (lane == 0) mbar_arrive(&p_full[j & 1]);
         }
         if (ok) ok = warp_wait(o_full, 0, abort_flag);
+        // join the halves (an abort is seen by all eight warps or comes too
+        // late to matter: the barrier below is reached either way)
+        ml[half * kBM + r] = make_float2(m, l);
+        named_bar_sync(1, kSoftmaxWarps * 32);
         if (ok) {
             tc_fence_after();
-            if (i < 0) l = 0.0f;  // no token of the sequence
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+            const float2 u0 = ml[r], u1 = ml[kBM + r];
+            const float top = fmaxf(u0.x, u1.x), base = top == -INFINITY ? 0.0f : top;
+            const float f0 = ex2(u0.x - base), f1 = ex2(u1.x - base);
+            const float sum = i >= 0 ? u0.y * f0 + u1.y * f1 : 0.0f;  // i < 0: no token of the sequence
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
             const size_t at = part ? (size_t)blockIdx.z * ((size_t)L * a.Hq) + orow : 0;
+            float o[32], o1[32];
+            tmem_ld32f(t_lane + kTmemO + half * 32, o);
+            tmem_ld32f(t_lane + kTmemO + kD + half * 32, o1);
+            tmem_ld_wait();
+            regs_ready<32>(o);
+            regs_ready<32>(o1);
+            // (a half that saw no key holds exact zeros)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float o[32];
-                tmem_ld32f(tO + h * 32, o);
-                tmem_ld_wait();
-                regs_ready<32>(o);
-                if (l == 0.0f) {  // a row with no key
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-                }
-                if (row_stored && part) {
-                    float4* d = reinterpret_cast<float4*>(pl.o + at * kD + h * 32);
+            for (int c = 0; c < 32; ++c) o[c] = sum == 0.0f ? 0.0f : o[c] * f0 + o1[c] * f1;
+            if (row_stored) {
+                if (part) {
+                    float4* d = reinterpret_cast<float4*>(pl.o + at * kD + half * 32);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         d[c] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
-                } else if (row_stored) {
-                    store_row32(static_cast<T*>(a.out) + orow * kD + h * 32, o, inv);
+                    if (half == 0) pl.lse[at] = lse2;
+                } else {
+                    store_row32(static_cast<T*>(a.out) + orow * kD + half * 32, o, inv);
+                    if constexpr (!kPaged) {
+                        if (half == 0) a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = lse2 * kLn2;
+                    }
                 }
-                __syncwarp();
-            }
-            if (row_stored) {
-                if (part) pl.lse[at] = lse2;
-                if constexpr (!kPaged) a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = lse2 * kLn2;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) record_status(a.status, 0, LF_ERR_DEVICE_TIMEOUT);
-    if (warp == 5) {
+    if (warp == kSoftmaxWarps + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }

@@ -395,29 +395,44 @@ def _encoder(fn_name, size_fn, x, local_mask, global_mask, layers, H, w, attn_sc
 # --------------------------------------------------------------------------
 # windowed causal attention with sinks, its paged form, layer norm
 # --------------------------------------------------------------------------
-@contextlib.contextmanager
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(first, stream, *tensors):
-    """The device of `first` current and `stream` (default: that device's
-    current one) the stream that outputs and workspaces are allocated on."""
-    if not first.is_cuda:
+    """A context in which the device of `first` is current and `stream` (if
+    given) the stream that outputs and workspaces are allocated on."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("expected a CUDA tensor")
     for t in tensors:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors on different devices: %s and %s" % (first.device, t.device))
-    if stream is not None and stream.device != first.device:
-        raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, first.device))
-    with torch.cuda.device(first.device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
+    if stream is not None:
+        if stream.device != first.device:
+            raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, first.device))
+        return torch.cuda.stream(stream)  # makes its device current too
+    return _HERE_ALREADY if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, tensor):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(tensor.get_device())
+
+
+def _dense(t):
+    """The address of a contiguous tensor (its device has been checked)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
 
 
 def _want(name, t, dtype=None, shape=None):
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
 
@@ -431,15 +446,14 @@ def _int32(**values):
 def _heads(name, t, dtype=None, shape=None):
     """lf_heads of [B, H, T, 64], or of packed [T, H, 64]."""
     _want(name, t, dtype, shape)
+    strides = t.stride()
     if t.dim() not in (3, 4) or t.shape[-1] != 64:
         raise ValueError("%s: expected [B, H, L, 64] or packed [T, H, 64], got %s" % (name, tuple(t.shape)))
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if t.numel() and t.stride(-1) != 1:
+    if strides[-1] != 1 and t.numel():
         raise ValueError("%s: the last dimension must be contiguous" % name)
-    if t.dim() == 3:
-        return ctypes.byref(Heads(t.data_ptr(), 0, t.stride(1), t.stride(0)))
-    return ctypes.byref(Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+    if len(strides) == 3:
+        return Heads(t.data_ptr(), 0, strides[1], strides[0])
+    return Heads(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
 def _window_shape(q, k, v, cu_seqlens, seq_lens):
@@ -483,8 +497,8 @@ def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 
         lse = (torch.empty(l_shape, dtype=torch.float32, device=q.device) if lse is None
                else _want("lse", lse, torch.float32, l_shape))
         st = lib().lf_window_attention_forward(
-            _heads("q", q), _heads("k", k), _heads("v", v), _ptr(cu_seqlens), _ptr(seq_lens), n, Hq, Hkv, L, w, sinks,
-            scale, DTYPE_CODE.get(q.dtype, 99), _stream(stream), _ptr(out), _ptr(lse))
+            _heads("q", q), _heads("k", k), _heads("v", v), _dense(cu_seqlens), _dense(seq_lens), n, Hq, Hkv, L, w, sinks,
+            scale, DTYPE_CODE.get(q.dtype, 99), _raw_stream(stream, q), _dense(out), _dense(lse))
     _check(st, "lf_window_attention_forward")
     return out, lse
 
@@ -513,9 +527,9 @@ def lf_window_attention_backward(q, k, v, out, lse, dout, w: int, sinks: int = 0
         if workspace is None:
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         st = lib().lf_window_attention_backward(
-            _heads("q", q), _heads("k", k), _heads("v", v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_seqlens),
-            _ptr(seq_lens), n, Hq, Hkv, L, w, sinks, scale, DTYPE_CODE.get(q.dtype, 99), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream), _heads("dq", dq, q.dtype, q.shape),
+            _heads("q", q), _heads("k", k), _heads("v", v), _dense(out), _dense(lse), _dense(dout), _dense(cu_seqlens),
+            _dense(seq_lens), n, Hq, Hkv, L, w, sinks, scale, DTYPE_CODE.get(q.dtype, 99), _dense(workspace),
+            workspace.numel() * workspace.element_size(), _raw_stream(stream, q), _heads("dq", dq, q.dtype, q.shape),
             _heads("dk", dk, q.dtype, k.shape), _heads("dv", dv, q.dtype, v.shape))
     _check(st, "lf_window_attention_backward")
     return dq, dk, dv
@@ -550,8 +564,8 @@ def lf_paged_cache_append(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_le
     with _on(k, stream, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
         st = lib().lf_paged_cache_append(
             _heads("k", k), _heads("v", v), _heads("k_cache", k_cache), _heads("v_cache", v_cache),
-            _ptr(block_table), _ptr(cu_seqlens), _ptr(kv_lens), n, Hkv, T, max_pages, num_pages, page_size,
-            DTYPE_CODE.get(k.dtype, 99), _stream(stream))
+            _dense(block_table), _dense(cu_seqlens), _dense(kv_lens), n, Hkv, T, max_pages, num_pages, page_size,
+            DTYPE_CODE.get(k.dtype, 99), _raw_stream(stream, k))
     _check(st, "lf_paged_cache_append")
 
 
@@ -577,10 +591,10 @@ def lf_paged_attention_forward(q, k_cache, v_cache, block_table, cu_seqlens, kv_
         if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         st = lib().lf_paged_attention_forward(
-            _heads("q", q), _heads("k_cache", k_cache), _heads("v_cache", v_cache), _ptr(block_table),
-            _ptr(cu_seqlens), _ptr(kv_lens), n, Hq, Hkv, T, max_q_len, max_pages, num_pages, page_size, w, sinks,
-            scale, DTYPE_CODE.get(q.dtype, 99), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream), _ptr(out))
+            _heads("q", q), _heads("k_cache", k_cache), _heads("v_cache", v_cache), _dense(block_table),
+            _dense(cu_seqlens), _dense(kv_lens), n, Hq, Hkv, T, max_q_len, max_pages, num_pages, page_size, w, sinks,
+            scale, DTYPE_CODE.get(q.dtype, 99), _dense(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, q), _dense(out))
     _check(st, "lf_paged_attention_forward")
     return out
 
@@ -588,17 +602,15 @@ def lf_paged_attention_forward(q, k_cache, v_cache, block_table, cu_seqlens, kv_
 def _rows(name, t):
     """(pointer, rows, N, row stride) of [..., N]: contiguous, or 2-D with a
     contiguous last dimension."""
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
     if t.dim() == 0:
         raise ValueError("%s: expected [..., N]" % name)
     N = t.shape[-1]
     rows = t.numel() // N if N else 0
     if t.dim() == 2 and (t.stride(1) == 1 or N == 1) and not t.is_contiguous():
-        return ctypes.c_void_p(t.data_ptr()), rows, N, t.stride(0)
+        return t.data_ptr(), rows, N, t.stride(0)
     if not t.is_contiguous():
         raise ValueError("%s: expected a contiguous tensor, or a 2-D one with a row stride" % name)
-    return ctypes.c_void_p(t.data_ptr()), rows, N, N
+    return t.data_ptr(), rows, N, N
 
 
 def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
@@ -613,9 +625,9 @@ def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None,
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else _want("out", out, x.dtype, x.shape)
         mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) if t is None
                       else _want(name, t, torch.float32, (rows,)) for name, t in (("mean", mean), ("rstd", rstd)))
-        st = lib().lf_layer_norm_forward(px, stride, _ptr(gamma), _ptr(beta), rows, N, eps,
-                                         DTYPE_CODE.get(x.dtype, 99), _stream(stream), _ptr(out), _ptr(mean),
-                                         _ptr(rstd))
+        st = lib().lf_layer_norm_forward(px, stride, _dense(gamma), _dense(beta), rows, N, eps,
+                                         DTYPE_CODE.get(x.dtype, 99), _raw_stream(stream, x), _dense(out), _dense(mean),
+                                         _dense(rstd))
     _check(st, "lf_layer_norm_forward")
     return out, mean, rstd
 
@@ -647,8 +659,8 @@ def lf_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta
             workspace = torch.empty(max(256, lf_layer_norm_backward_workspace_bytes(rows, N)), dtype=torch.uint8,
                                     device=x.device)
         st = lib().lf_layer_norm_backward(
-            pdy, dys, px, xs, _ptr(gamma), _ptr(mean), _ptr(rstd), rows, N, DTYPE_CODE.get(x.dtype, 99),
-            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(stream), _ptr(dx), _ptr(dgamma), _ptr(dbeta))
+            pdy, dys, px, xs, _dense(gamma), _dense(mean), _dense(rstd), rows, N, DTYPE_CODE.get(x.dtype, 99),
+            _dense(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _raw_stream(stream, x), _dense(dx), _dense(dgamma), _dense(dbeta))
     _check(st, "lf_layer_norm_backward")
     return dx, dgamma, dbeta

@@ -100,6 +100,13 @@ def test_longer_sequences(dtype):
     _packed([1500], 2, 2, 1 << 30, 0, dtype, seed=6)
 
 
+@pytest.mark.parametrize("Hq,Hkv,w", [(16, 16, 256), (16, 4, 700)])
+def test_a_full_grid(Hq, Hkv, w):
+    """More tiles than the GPU holds at once, several blocks each: every
+    CTA's roles run at their own pace (the device status word stays clear)."""
+    _packed([4096, 3001], Hq, Hkv, w, 4, "f16", seed=7)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_many_short_sequences(dtype):
     lens = [(7 * i * i + 3 * i) % 40 for i in range(70)]
