@@ -13,7 +13,7 @@ constexpr int kRowsPerBlock = 32;
 __global__ void __launch_bounds__(kRowsPerBlock * 8) append_kernel(const __grid_constant__ PagedArgs a) {
     const int part = threadIdx.x & 7;
     const long long row = (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 3);  // (token, kv head)
-    if (blockIdx.x == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status);
+    if (blockIdx.x == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status, threadIdx.x, blockDim.x);
     if (row >= (long long)a.T * a.Hkv) return;
     const int tok = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
     const int b = seq_of_token(a.cu, a.n_seqs, tok);

@@ -61,7 +61,7 @@ decode_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Paged
     const int b = blockIdx.x / pl.decode_splits, piece = blockIdx.x % pl.decode_splits, hk = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status);
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status, threadIdx.x, blockDim.x);
     const int start = iclamp(a.cu[b], 0, a.T), n = iclamp(a.cu[b + 1], 0, a.T) - start, G = a.Hq / a.Hkv;
     int kv, first;
     if (n <= 0 || !paged_seq(a, b, n, kv, first, threadIdx.x == 0 && hk == 0 && piece == 0)) return;

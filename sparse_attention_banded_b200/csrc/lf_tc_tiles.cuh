@@ -60,14 +60,51 @@ __device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&r)[16])
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// The tensor-core instructions of a whole warp, issued by its elected lane.
+// One asm block holds the four k-steps of a product: issued one by one from
+// a lane's branch, each instruction's descriptors were moved to uniform
+// registers again, about 120 cycles apiece (640 cycles for four MMAs and a
+// commit of the attention kernel's issuing warp, 320 in this form).
+
+// D[tmem] (+)= A B^T over 64 of K: A (128 rows) and B (64 rows) K-major in
+// shared memory, 128-byte swizzle.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate = 0) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D0 (+)= A[:, :32] B[:32], D1 (+)= A[:, 32:] B[32:]: A (128 x 64, 16-bit) in
+// tensor memory, its halves of 32 in 16 columns each, 32 columns apart; B 64
+// x 64, MN-major in shared memory.  D1 == D0 with accumulate_second: one sum.
+__device__ __forceinline__ void mma4_ts(uint32_t d0, uint32_t d1, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t accumulate_second) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q, r;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 r, %6, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "add.s32 a1, %2, 8;\n\tadd.s32 a2, %2, 32;\n\tadd.s32 a3, %2, 40;\n\t"
+        "add.s64 b1, %3, 128;\n\tadd.s64 b2, %3, 256;\n\tadd.s64 b3, %3, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %3, %4, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [a2], b2, %4, r;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [a3], b3, %4, q;\n\t}" ::"r"(d0),
+        "r"(d1), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(accumulate_second)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 
@@ -94,25 +131,18 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-#ifndef LF_HINT
-#define LF_HINT 10000
-#endif
-// mbarrier test that may suspend the thread for up to `hint_ns`.
-__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-        : "memory");
-    return ok != 0;
-}
-// The whole warp waits (bounded, as mbar_wait); the result is warp-uniform.
+// The whole warp waits; the result is warp-uniform.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, LF_HINT))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Half a row: 32 16-bit values from 32 floats.

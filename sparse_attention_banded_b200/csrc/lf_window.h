@@ -78,9 +78,11 @@ __device__ __forceinline__ bool paged_seq(const PagedArgs& a, int b, int n, int&
 }
 
 // The offsets must ascend from 0 to at most L, and lengths fit; records the
-// sequences whose do not (every access is clamped anyway).  One block calls.
-__device__ __forceinline__ void check_lengths(const int32_t* cu, const int32_t* lens, int n_seqs, int L, int* status) {
-    for (int b = threadIdx.x; b < n_seqs; b += blockDim.x) {
+// sequences whose do not (every access is clamped anyway).  Called by one
+// group of `step` threads.
+__device__ __forceinline__ void check_lengths(const int32_t* cu, const int32_t* lens, int n_seqs, int L, int* status,
+                                              int thread, int step) {
+    for (int b = thread; b < n_seqs; b += step) {
         const bool bad = cu ? (cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > L) : (lens && (lens[b] < 0 || lens[b] > L));
         if (bad) record_status(status, b, LF_ERR_BAD_LENGTHS);
     }

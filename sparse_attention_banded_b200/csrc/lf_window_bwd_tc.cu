@@ -100,7 +100,7 @@ __device__ __forceinline__ Ctx setup(uint8_t* smem, int warp, int lane) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    c.tmem = *slot;
+    c.tmem = __shfl_sync(0xffffffffu, *slot, 0);
     return c;
 }
 
@@ -123,27 +123,20 @@ __device__ __forceinline__ void drain_loads(const Ctx& c, int issued) {
 }
 __device__ __forceinline__ void drain_mmas(const Ctx& c) {
     volatile int never = 0;
-    tc_commit(c.drain);
+    commit_elect(c.drain);
     mbar_wait(c.drain, 0, &never, 200000000ull);
 }
 
 // D = A B^T, both 64 wide and K-major in shared memory (M 128, N 64).
 template <typename T>
 __device__ __forceinline__ void mma_nt(uint32_t d, uint32_t a_smem, uint32_t b_smem) {
-    constexpr uint32_t id = idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 0);
-    const uint64_t da = desc_sw128(a_smem), db = desc_sw128(b_smem);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f16_ss(d, da + k * 2, db + k * 2, id, k > 0);
+    mma4_ss(d, desc_sw128(a_smem), desc_sw128(b_smem), idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 0));
 }
 // D += A B: A (128 x 64, 16-bit) in tensor memory, its halves 32 columns
 // apart; B 64 x 64 in shared memory.
 template <typename T>
 __device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a_tmem, uint32_t b_smem, bool accumulate) {
-    constexpr uint32_t id = idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 1);
-    const uint64_t db = desc_sw128(b_smem, 0);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        mma_f16_ts(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, db + k * (2048 >> 4), id, accumulate || k > 0);
+    mma4_ts(d, d, a_tmem, desc_sw128(b_smem, 0), idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 1), accumulate, 1);
 }
 
 // exp2 of a pair; in a tile without masked scores a third run on the FMA pipe.
@@ -174,7 +167,7 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
     pdl_launch_dependents();
     pdl_wait();
     const int G = a.Hq / a.Hkv, TQ = 128 / G, hk = blockIdx.y;
-    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status);
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status, threadIdx.x, blockDim.x);
     // long rows of a causal sequence first
     const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, gridDim.x - 1 - blockIdx.x);
     if (t.t0 >= t.rows) return;
@@ -229,12 +222,9 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
             if (!warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag)) return false;
             if (j > 0 && !warp_wait(c.free_, (j - 1) & 1, c.abort_flag)) return false;
             tc_fence_after();
-            if (lane == 0) {
-                mma_nt<T>(tmS + (j & 1) * 64, smem_u32(smem), b0 + s * 2 * kSmall);
-                mma_nt<T>(tmP, smem_u32(smem + kBig), b0 + s * 2 * kSmall + kSmall);
-                tc_commit(c.s_full);
-            }
-            __syncwarp();
+            mma_nt<T>(tmS + (j & 1) * 64, smem_u32(smem), b0 + s * 2 * kSmall);
+            mma_nt<T>(tmP, smem_u32(smem + kBig), b0 + s * 2 * kSmall + kSmall);
+            commit_elect(c.s_full);
             return true;
         };
         ok = ok && scores(0);
@@ -243,14 +233,11 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
             ok = ok && warp_wait(&c.ready[j & 1], (j >> 1) & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                mma_tn<T>(tmQ, tmS + (j & 1) * 64, b0 + (j % kStages) * 2 * kSmall, j > 0);
-                tc_commit(&c.b_empty[j % kStages]);
-                if (j == kb.n - 1) tc_commit(c.done);
-            }
-            __syncwarp();
+            mma_tn<T>(tmQ, tmS + (j & 1) * 64, b0 + (j % kStages) * 2 * kSmall, j > 0);
+            commit_elect(&c.b_empty[j % kStages]);
+            if (j == kb.n - 1) commit_elect(c.done);
         }
-        if (!ok && lane == 0) drain_mmas(c);
+        if (!ok) drain_mmas(c);
     } else {
         // ------------------------------------------------------------ math
         // delta: two threads a row, 32 products each
@@ -440,24 +427,18 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
             ok = warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                mma_nt<T>(tmS, smem_u32(smem), bq);
-                mma_nt<T>(tmP, smem_u32(smem + kBig), bo);
-                tc_commit(c.s_full);
-            }
-            __syncwarp();
+            mma_nt<T>(tmS, smem_u32(smem), bq);
+            mma_nt<T>(tmP, smem_u32(smem + kBig), bo);
+            commit_elect(c.s_full);
             ok = warp_wait(&c.ready[0], j & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-                mma_tn<T>(tmV, tmS, bo, j > 0);
-                mma_tn<T>(tmK, tmP, bq, j > 0);
-                tc_commit(&c.b_empty[s]);
-                if (j == nq - 1) tc_commit(c.done);
-            }
-            __syncwarp();
+            mma_tn<T>(tmV, tmS, bo, j > 0);
+            mma_tn<T>(tmK, tmP, bq, j > 0);
+            commit_elect(&c.b_empty[s]);
+            if (j == nq - 1) commit_elect(c.done);
         }
-        if (!ok && lane == 0) drain_mmas(c);
+        if (!ok) drain_mmas(c);
     } else {
         // ------------------------------------------------------------ math
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + kTile, *V = K + kTile, *P = V + kTile;
     const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
-    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status);
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status, threadIdx.x, blockDim.x);
     const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, blockIdx.x);
     if (t.t0 >= t.rows) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ Wi
     extern __shared__ float sm[];
     float *Q = sm, *dO = Q + kTile, *K = dO + kTile, *V = K + kTile, *S = V + kTile;
     const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
-    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status);
+    if (blockIdx.x == 0 && hk == 0) check_lengths(a.cu, a.lens, a.n_seqs, a.L, a.status, threadIdx.x, blockDim.x);
     const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, TQ, blockIdx.x);
     if (t.t0 >= t.rows) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;

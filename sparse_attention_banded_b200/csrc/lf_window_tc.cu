@@ -1,30 +1,34 @@
 // Windowed causal attention with sinks, forward, on the sm_100a tensor cores
 // (fp16 / bf16): over packed or padded sequences, or over a paged cache.
 //
-// One CTA per tile of 128 query rows: 128 / G tokens times the G query heads
-// that share a key/value head, so grouped heads read each key block once and
-// a tile's keys span only w + 128 / G positions.  Per block of 64 keys:
+// A persistent CTA works on tiles of 128 query rows: 128 / G tokens times the
+// G query heads that share a key/value head, so grouped heads read each key
+// block once and a tile's keys span only w + 128 / G positions.  Per block of
+// 64 keys:
 //     S = Q K^T                        (tcgen05.mma, fp32 in tensor memory)
 //     m' = max(m, max s), P = 2^(s - m'), l += sum P
 //     O = O 2^(m - m') + P V           (P from tensor memory)
 // Two threads share a row, each with its own half of every block's keys, its
 // own m, l and O: they meet only at the tile's end, as two pieces of a split
 // context would.  S has two buffers, so the next block's S runs under this
-// one's softmax and the softmax warps never wait for a product; P overwrites
-// the first 16 columns of its half of S.  S, S and two O's take 256 tensor-
-// memory columns: two CTAs per SM.  (One thread a row, one S buffer and four
-// CTAs per SM left every CTA a chain of latencies: 195 us at 16384 packed
-// tokens, 16 / 4 heads, window 1024, 37 % of the issue slots used.)
+// one's softmax; P overwrites the first 16 columns of its half of S.  S, S
+// and two O's take 256 tensor-memory columns: two CTAs per SM.  A block
+// takes a CTA about 2000 cycles, 800 of them arithmetic and the rest the
+// latencies of tensor-memory accesses and hand-offs, which the other CTA's
+// warps fill; a tile of its own launch paid 8000 cycles more to start and
+// end, so the loads, the plan and the first S of the next tile run under the
+// end of this one.
 // The O update is skipped unless a row's maximum grows by more than 2^8 (P
 // <= 2^8 then).  P is rounded to the storage type, the MMA's operand type;
 // sums stay fp32.
 //
-// Warps 0-7: softmax and epilogue, warp 8: TMA loads, warp 9: MMAs.  All
-// waits are bounded (LF_ERR_DEVICE_TIMEOUT).
+// Warps 0-7: softmax and epilogue, warp 8: TMA loads, warp 9: MMAs, warp 10:
+// the plans of the coming tiles (which sequence, which keys).  All waits are
+// bounded (LF_ERR_DEVICE_TIMEOUT).
 //
 // Paged: a block is gathered by one TMA box per page (of up to 64
-// positions).  Long contexts of few tiles are split over gridDim.z CTAs of
-// `per` blocks each, which leave normalised fp32 rows and their log2-sum-exp
+// positions).  Long contexts of few tiles are split into items of `per`
+// blocks each, which leave normalised fp32 rows and their log2-sum-exp
 // for the merge kernel.
 #include <atomic>
 #include <mutex>
@@ -73,14 +77,21 @@ using namespace sm100;
 constexpr int kBM = 128;   // query rows
 constexpr int kBN = 64;    // keys per block
 constexpr int kD = 64;
-constexpr int kStages = 3;
+constexpr int kStages = 4;
+constexpr int kRing = 4;   // plans ahead
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
+constexpr int kThreads = 12 * 32;
 constexpr int kCtas = 2;   // per SM
+// 80 registers a thread at launch; a block's share is split anew.
+constexpr uint32_t kRegsLaunch = 80, kRegsProducer = 48, kRegsSoftmax = 96;
+static_assert(4 * 32 * kRegsProducer + 8 * 32 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kQBytes = kBM * kD * 2, kKBytes = kBN * kD * 2;
-constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffMl = kOffV + kStages * kKBytes;
-constexpr uint32_t kOffBar = kOffMl + 2 * kBM * 8;               // (m, l) of both halves
-constexpr uint32_t kBars = 1 + 3 * kStages + 7;
+constexpr uint32_t kOffK = 2 * kQBytes, kOffV = kOffK + kStages * kKBytes, kOffMl = kOffV + kStages * kKBytes;
+constexpr uint32_t kOffPlan = kOffMl + 2 * kBM * 8;              // after (m, l) of both halves
+constexpr uint32_t kPlanBytes = 80;
+constexpr uint32_t kOffBar = kOffPlan + kRing * kPlanBytes;
+constexpr uint32_t kBars = 4 + 2 * kStages + 7 + 2 * kRing;
 constexpr uint32_t kOffMask = kOffBar + kBars * 8;               // valid keys of each stage (paged)
 constexpr uint32_t kOffMisc = kOffMask + kStages * 8;
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;            // + alignment slack
@@ -93,20 +104,91 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
+// What a tile's roles need to know; nb = 0: rows of zeros (padding, or
+// nothing to see), nb < 0: no more tiles.
+struct Plan {
+    int nb, b0, n_sink, lo;    // blocks [b0, b0 + nb) of the list n_sink, lo
+    int i0, i1, n_keys;        // positions of its tokens, keys of the sequence
+    int first;                 // position of the sequence's first token
+    int b, batch, start, t0;   // sequence, its batch and first row; the tile's first token
+    int n, rows, hk;           // tokens, stored rows of the sequence; key/value head
+    int part, z;               // one piece of several: index
+    __device__ __forceinline__ int key0(int j) const {  // first key of the tile's j-th block
+        j += b0;
+        return (j < n_sink ? j : lo + (j - n_sink)) * kBN;
+    }
+};
+static_assert(sizeof(Plan) <= kPlanBytes, "plan slot");
+
+template <bool kPaged, typename A>
+__device__ __forceinline__ int rows_total(const A& a) {
+    if constexpr (kPaged) return a.T;
+    else return a.L;
+}
+
+// The plan of an item; false: the item has no work at all.
+template <bool kPaged, typename A>
+__device__ bool make_plan(const A& a, const PagedPlan& pp, int item, Plan& p, bool report) {
+    const int G = a.Hq / a.Hkv, TQ = kBM / G;
+    int slot = item, z = 0;
+    if constexpr (kPaged) {
+        z = slot % pp.tensor_splits;
+        slot /= pp.tensor_splits;
+    }
+    p.hk = slot % a.Hkv;
+    slot /= a.Hkv;
+    const int32_t* lens = nullptr;
+    if constexpr (!kPaged) lens = a.lens;
+    const TokenTile t = token_tile(a.cu, lens, a.n_seqs, rows_total<kPaged>(a), TQ, slot);
+    if (t.t0 >= t.rows) return false;
+    p.first = 0;
+    p.n_keys = t.n;
+    if constexpr (kPaged) {
+        if (pp.decode && t.n * G <= kDecodeRows) return false;  // the decode kernel's
+        if (!paged_seq(a, t.b, t.n, p.n_keys, p.first, report && p.hk == 0 && z == 0 && t.t0 == 0)) return false;
+    }
+    const int t1 = imin(t.t0 + TQ, t.n);
+    const KeyBlocks kb = tile_key_blocks(p.first, t.t0, t1, p.n_keys, a.w, a.sinks);
+    p.i0 = p.first + t.t0;
+    p.i1 = p.first + t1 - 1;
+    p.n_sink = kb.n_sink;
+    p.lo = kb.lo;
+    p.b0 = 0;
+    p.nb = kb.n;
+    p.part = 0;
+    p.z = z;
+    if constexpr (kPaged) {
+        p.b0 = imin(z * pp.per, kb.n);
+        p.nb = imin(p.b0 + pp.per, kb.n) - p.b0;
+        p.part = kb.n > pp.per;
+        if (p.nb == 0 && z > 0) return false;
+    }
+    p.b = t.b;
+    p.batch = t.batch;
+    p.start = t.start;
+    p.t0 = t.t0;
+    p.n = t.n;
+    p.rows = t.rows;
+    return true;
+}
+
 template <typename T, bool kPaged, typename A>
 __global__ void __launch_bounds__(kThreads, kCtas)
-window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, const __grid_constant__ PagedPlan pl) {
+window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, const __grid_constant__ PagedPlan pp,
+              int n_items) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
-    uint64_t* k_full = q_full + 1;
-    uint64_t* v_full = k_full + kStages;
-    uint64_t* kv_empty = v_full + kStages;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // [2]
+    uint64_t* q_empty = q_full + 2;                                  // [2]
+    uint64_t* kv_full = q_empty + 2;
+    uint64_t* kv_empty = kv_full + kStages;
     uint64_t* s_full = kv_empty + kStages;
     uint64_t* p_full = s_full + 2;  // (both [2]: per S buffer)
-    uint64_t* pv_done = p_full + 2;
-    uint64_t* o_full = pv_done + 1;
-    uint64_t* drain = o_full + 1;
+    uint64_t* o_full = p_full + 2;
+    uint64_t* ml_full = o_full + 1;
+    uint64_t* drain = ml_full + 1;
+    uint64_t* plan_full = drain + 1;
+    uint64_t* plan_empty = plan_full + kRing;
     float2* ml = reinterpret_cast<float2*>(smem + kOffMl);
     volatile unsigned long long* valid = reinterpret_cast<volatile unsigned long long*>(smem + kOffMask);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -114,344 +196,391 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
-    pdl_wait();
-    const int G = a.Hq / a.Hkv, TQ = kBM / G, hk = blockIdx.y;
-    int L;
-    if constexpr (kPaged) L = a.T;
-    else L = a.L;
-    const int32_t* lens = nullptr;
-    if constexpr (!kPaged) lens = a.lens;
-    if (blockIdx.x == 0 && hk == 0 && blockIdx.z == 0) check_lengths(a.cu, lens, a.n_seqs, L, a.status);
-    const TokenTile t = token_tile(a.cu, lens, a.n_seqs, L, TQ, blockIdx.x);
-    if (t.t0 >= t.rows) return;
-    int first = 0, n_keys = t.n;  // position of the first token, keys in all
-    if constexpr (kPaged) {
-        if (pl.decode && t.n * G <= kDecodeRows) return;  // the decode kernel's
-        if (!paged_seq(a, t.b, t.n, n_keys, first, threadIdx.x == 0 && hk == 0 && blockIdx.z == 0 && t.t0 == 0)) return;
-    }
-    const int i0 = first + t.t0, i1 = first + imin(t.t0 + TQ, t.n) - 1;  // positions of the tile's tokens
-    const KeyBlocks kb = tile_key_blocks(first, t.t0, imin(t.t0 + TQ, t.n), n_keys, a.w, a.sinks);
-    int b0 = 0, b1 = kb.n;
-    bool part = false;  // one piece of several
-    if constexpr (kPaged) {
-        b0 = imin(blockIdx.z * pl.per, kb.n);
-        b1 = imin(b0 + pl.per, kb.n);
-        part = kb.n > pl.per;
-        if (b0 == b1 && blockIdx.z > 0) return;
-    }
-    const int nb = b1 - b0;
-
-    // this thread's row and half (softmax warps)
-    const int r = (warp & 3) * 32 + lane, half = warp >> 2, tok = t.t0 + r / G, head = hk * G + r % G;
-    const bool row_stored = r < TQ * G && tok < t.rows;
-    const size_t orow = ((size_t)t.batch * L + t.start + tok) * a.Hq + head;
-
-    if (nb == 0) {  // padding, or nothing to see: zeros
-        if (half > 0 || !row_stored) return;
-        if constexpr (!kPaged) {
-            a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = -INFINITY;
-        }
-        zero_row64(static_cast<T*>(a.out) + orow * kD);
-        return;
-    }
-
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(&q_full[u], 1);
+            mbar_init(&q_empty[u], 1);
+            mbar_init(&s_full[u], 1);
+            mbar_init(&p_full[u], kSoftmaxWarps);
+        }
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&k_full[s], 1);
-            mbar_init(&v_full[s], 1);
+            mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
         }
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
-        mbar_init(&p_full[0], kSoftmaxWarps);
-        mbar_init(&p_full[1], kSoftmaxWarps);
-        mbar_init(pv_done, 1);
         mbar_init(o_full, 1);
+        mbar_init(ml_full, kSoftmaxWarps);
         mbar_init(drain, 1);
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&plan_full[s], 1);
+            mbar_init(&plan_empty[s], kSoftmaxWarps + 2);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kSoftmaxWarps + 1) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
-    }
-    if (warp == kSoftmaxWarps && lane == 0) {
+    if (warp == kTmaWarp && lane == 0) {
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);
     }
+    // (only now: a kernel that runs before may hold tensor memory until it ends)
+    pdl_wait();
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const int G = a.Hq / a.Hkv, TQ = kBM / G, L = rows_total<kPaged>(a);
 
-    if (warp == kSoftmaxWarps) {
-        // ------------------------------------------------------------ TMA
-        bool ok = true;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, (uint32_t)(TQ * G) * kD * 2);
-            tma_load_4d(smem, &maps.q, q_full, 0, hk * G, t.start + t.t0, t.batch);
+    // The plans, in order; the slot of plan k - 1 is handed back when the
+    // role asks for plan k.  NULL after an abort.
+    auto next_plan = [&](int k) -> const Plan* {
+        if (k > 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&plan_empty[(k - 1) % kRing]);
         }
-        int j = 0;
-        for (; j < nb; ++j) {
-            const int s = j % kStages;
-            ok = warp_wait(&kv_empty[s], ((j / kStages) & 1) ^ 1, abort_flag);
-            if (!ok) break;
-            const int c0 = key_block(kb, b0 + j) * kBN;
-            uint8_t *ks = smem + kOffK + s * kKBytes, *vs = smem + kOffV + s * kKBytes;
-            if constexpr (kPaged) {
-                // lane u fetches the box of the block's u-th page
-                const int shift = a.page_shift, rows = imin(kBN, 1 << shift), boxes = kBN / rows;
-                const int pos = c0 + lane * rows;
-                int page = -1;
-                if (lane < boxes && pos < n_keys) {
-                    page = page_of(a.table + (size_t)t.b * a.max_pages, a.max_pages, a.num_pages, shift, pos);
-                    if (page < 0 && range_visible(imax(i0, 0), i1, pos, imin(pos + rows, n_keys) - 1, a.w, a.sinks))
-                        record_status(a.status, t.b, LF_ERR_BAD_PAGE);
-                }
-                const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+        if (!warp_wait(&plan_full[k % kRing], (k / kRing) & 1, abort_flag)) return nullptr;
+        return reinterpret_cast<const Plan*>(smem + kOffPlan + (k % kRing) * kPlanBytes);
+    };
+
+    if (warp >= kSoftmaxWarps) {
+        regs_dec<kRegsProducer>();
+        if (warp == kPlanWarp) {
+            // -------------------------------------------------------- plans
+            const int32_t* lens = nullptr;
+            if constexpr (!kPaged) lens = a.lens;
+            if (blockIdx.x == 0) check_lengths(a.cu, lens, a.n_seqs, L, a.status, lane, 32);
+            int k = 0;
+            for (int item = blockIdx.x;; item += gridDim.x) {
+                Plan p;
+                p.nb = -1;
+                if (item < n_items && !make_plan<kPaged>(a, pp, item, p, lane == 0)) continue;
+                if (!warp_wait(&plan_empty[k % kRing], ((k / kRing) & 1) ^ 1, abort_flag)) break;
                 if (lane == 0) {
-                    unsigned long long m = 0;
-                    for (int u = 0; u < boxes; ++u)
-                        if ((have >> u) & 1) m |= low_bits64(rows) << (u * rows);
-                    // and only keys some row sees: others' values may be anything
-                    valid[s] = m & low_bits64(imin(n_keys, i1 + 1) - c0) &
-                               (~low_bits64(imax(i0, 0) - a.w - c0) | low_bits64(a.sinks - c0));
-                    const uint32_t bytes = __popc(have) * rows * kD * 2;
-                    if (bytes) {
-                        mbar_arrive_expect_tx(&k_full[s], bytes);
-                        mbar_arrive_expect_tx(&v_full[s], bytes);
+                    *reinterpret_cast<Plan*>(smem + kOffPlan + (k % kRing) * kPlanBytes) = p;
+                    mbar_arrive(&plan_full[k % kRing]);
+                }
+                ++k;
+                if (p.nb < 0) break;
+            }
+        } else if (warp == kTmaWarp) {
+            // -------------------------------------------------------- TMA
+            bool ok = true;
+            int g = 0, it = 0;  // blocks, tiles with blocks so far
+            for (int k = 0; ok; ++k) {
+                const Plan* p = next_plan(k);
+                if (!p || p->nb < 0) {
+                    ok = p != nullptr;
+                    break;
+                }
+                if (p->nb == 0) continue;
+                ok = warp_wait(&q_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[it & 1], (uint32_t)(TQ * G) * kD * 2);
+                    tma_load_4d(smem + (it & 1) * kQBytes, &maps.q, &q_full[it & 1], 0, p->hk * G, p->start + p->t0, p->batch);
+                }
+                ++it;
+                const int hk = p->hk, n_keys = p->n_keys, nb = p->nb;
+                for (int j = 0; j < nb; ++j, ++g) {
+                    const int s = g % kStages;
+                    const int c0 = p->key0(j);
+                    uint8_t *ks = smem + kOffK + s * kKBytes, *vs = smem + kOffV + s * kKBytes;
+                    if constexpr (kPaged) {
+                        // lane u fetches the box of the block's u-th page
+                        const int shift = a.page_shift, rows = imin(kBN, 1 << shift), boxes = kBN / rows;
+                        const int pos = c0 + lane * rows, i0 = imax(p->i0, 0), i1 = p->i1;
+                        int page = -1;
+                        if (lane < boxes && pos < n_keys) {
+                            page = page_of(a.table + (size_t)p->b * a.max_pages, a.max_pages, a.num_pages, shift, pos);
+                            if (page < 0 && range_visible(i0, i1, pos, imin(pos + rows, n_keys) - 1, a.w, a.sinks))
+                                record_status(a.status, p->b, LF_ERR_BAD_PAGE);
+                        }
+                        const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+                        ok = warp_wait(&kv_empty[s], ((g / kStages) & 1) ^ 1, abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            unsigned long long m = 0;
+                            for (int u = 0; u < boxes; ++u)
+                                if ((have >> u) & 1) m |= low_bits64(rows) << (u * rows);
+                            // and only keys some row sees: others' values may be anything
+                            valid[s] = m & low_bits64(imin(n_keys, i1 + 1) - c0) &
+                                       (~low_bits64(i0 - a.w - c0) | low_bits64(a.sinks - c0));
+                            const uint32_t bytes = __popc(have) * rows * kD * 2;
+                            if (bytes) mbar_arrive_expect_tx(&kv_full[s], 2 * bytes);
+                            else mbar_arrive(&kv_full[s]);
+                        }
+                        __syncwarp();
+                        if (page >= 0) {
+                            const int slot = pos & ((1 << shift) - 1);
+                            tma_load_4d(ks + lane * rows * kD * 2, &maps.k, &kv_full[s], 0, hk, slot, page);
+                            tma_load_4d(vs + lane * rows * kD * 2, &maps.v, &kv_full[s], 0, hk, slot, page);
+                        }
+                        __syncwarp();
                     } else {
-                        mbar_arrive(&k_full[s]);
-                        mbar_arrive(&v_full[s]);
+                        ok = warp_wait(&kv_empty[s], ((g / kStages) & 1) ^ 1, abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&kv_full[s], 2 * kKBytes);
+                            tma_load_4d(ks, &maps.k, &kv_full[s], 0, hk, p->start + c0, p->batch);
+                            tma_load_4d(vs, &maps.v, &kv_full[s], 0, hk, p->start + c0, p->batch);
+                        }
+                        __syncwarp();
                     }
                 }
-                __syncwarp();
-                if (page >= 0) {
-                    const int slot = pos & ((1 << shift) - 1);
-                    tma_load_4d(ks + lane * rows * kD * 2, &maps.k, &k_full[s], 0, hk, slot, page);
-                    tma_load_4d(vs + lane * rows * kD * 2, &maps.v, &v_full[s], 0, hk, slot, page);
+            }
+            if (!ok && lane == 0) {  // wind-down: let issued copies land
+                volatile int never = 0;
+                for (int c = it > 2 ? it - 2 : 0; c < it; ++c) mbar_wait(&q_full[c & 1], (c >> 1) & 1, &never, 200000000ull);
+                for (int c = g > kStages ? g - kStages : 0; c < g; ++c)
+                    mbar_wait(&kv_full[c % kStages], (c / kStages) & 1, &never, 200000000ull);
+            }
+        } else if (warp == kMmaWarp) {
+            // -------------------------------------------------------- MMA
+            // In issue order S_0, S_1, PV_0, S_2, PV_1, ...: the products run
+            // in that order, so S of block g + 1 may overwrite P of block
+            // g - 1 without a wait.  The first PV of a tile overwrites O: it
+            // waits for the P of warps that have read the last tile's O.
+            constexpr uint32_t id_s = idesc_f16(MmaFormat<T>::fmt, kBM, kBN, 0, 0);
+            constexpr uint32_t id_o = idesc_f16(MmaFormat<T>::fmt, kBM, kD, 0, 1);
+            const uint64_t dq = desc_sw128(smem_u32(smem)), dk = desc_sw128(smem_u32(smem + kOffK)),
+                           dv = desc_sw128(smem_u32(smem + kOffV), 0);
+            bool ok = true;
+            int g = 0, it = 0;
+            for (int k = 0; ok; ++k) {
+                const Plan* p = next_plan(k);
+                if (!p || p->nb < 0) {
+                    ok = p != nullptr;
+                    break;
                 }
-                __syncwarp();
-            } else if (lane == 0) {
-                mbar_arrive_expect_tx(&k_full[s], kKBytes);
-                tma_load_4d(ks, &maps.k, &k_full[s], 0, hk, t.start + c0, t.batch);
-                mbar_arrive_expect_tx(&v_full[s], kKBytes);
-                tma_load_4d(vs, &maps.v, &v_full[s], 0, hk, t.start + c0, t.batch);
+                const int nb = p->nb;
+                if (nb == 0) continue;
+                auto scores = [&](int j) -> bool {
+                    const int s = (g + j) % kStages, buf = (g + j) & 1;
+                    if (!warp_wait(&kv_full[s], ((g + j) / kStages) & 1, abort_flag)) return false;
+                    tc_fence_after();
+                    mma4_ss(tmem + buf * kBN, dq + (it & 1) * (kQBytes >> 4), dk + s * (kKBytes >> 4), id_s);
+                    commit_elect(&s_full[buf]);
+                    if (j == nb - 1) commit_elect(&q_empty[it & 1]);
+                    return true;
+                };
+                ok = warp_wait(&q_full[it & 1], (it >> 1) & 1, abort_flag) && scores(0);
+                for (int j = 0; j < nb && ok; ++j) {
+                    const int c = g + j, s = c % kStages;
+                    // S of block j + 1 reuses the buffer of P of j - 1: its PV has been issued
+                    if (j + 1 < nb) ok = scores(j + 1);
+                    ok = ok && warp_wait(&p_full[c & 1], (c >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // half 0's keys into its O, half 1's into the other
+                    mma4_ts(tmem + kTmemO, tmem + kTmemO + kD, tmem + (c & 1) * kBN, dv + s * (kKBytes >> 4), id_o, j > 0,
+                            j > 0);
+                    commit_elect(&kv_empty[s]);
+                    if (j == nb - 1) commit_elect(o_full);
+                }
+                g += nb;
+                ++it;
             }
-        }
-        if (!ok && lane == 0) {  // wind-down: let issued copies land
-            volatile int never = 0;
-            mbar_wait(q_full, 0, &never, 200000000ull);
-            for (int c = j > kStages ? j - kStages : 0; c < j; ++c) {
-                mbar_wait(&k_full[c % kStages], (c / kStages) & 1, &never, 200000000ull);
-                mbar_wait(&v_full[c % kStages], (c / kStages) & 1, &never, 200000000ull);
+            if (!ok) {  // wind-down: wait for the MMAs already issued
+                volatile int never = 0;
+                commit_elect(drain);
+                mbar_wait(drain, 0, &never, 200000000ull);
             }
-        }
-    } else if (warp == kSoftmaxWarps + 1) {
-        // ------------------------------------------------------------ MMA
-        // In issue order S_0, S_1, PV_0, S_2, PV_1, ...: the products run in
-        // that order, so S_(j+1) may overwrite P_(j-1) without a wait.
-        constexpr uint32_t id_s = idesc_f16(MmaFormat<T>::fmt, kBM, kBN, 0, 0);
-        constexpr uint32_t id_o = idesc_f16(MmaFormat<T>::fmt, kBM, kD, 0, 1);
-        const uint64_t dq = desc_sw128(smem_u32(smem)), dk = desc_sw128(smem_u32(smem + kOffK)),
-                       dv = desc_sw128(smem_u32(smem + kOffV), 0);
-        auto scores = [&](int j) -> bool {
-            const int s = j % kStages;
-            if (!warp_wait(&k_full[s], (j / kStages) & 1, abort_flag)) return false;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk)
-                    mma_f16_ss(tmem + (j & 1) * kBN, dq + kk * 2, dk + s * (kKBytes >> 4) + kk * 2, id_s, kk > 0);
-                tc_commit(&s_full[j & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = warp_wait(q_full, 0, abort_flag) && scores(0);
-        for (int j = 0; j < nb && ok; ++j) {
-            const int s = j % kStages;
-            // S_(j+1) reuses the buffer of P_(j-1): its PV has been issued
-            if (j + 1 < nb) ok = scores(j + 1);
-            ok = ok && warp_wait(&v_full[s], (j / kStages) & 1, abort_flag) &&
-                 warp_wait(&p_full[j & 1], (j >> 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)  // two steps of 16 keys for each half's O
-                    mma_f16_ts(tmem + kTmemO + (kk >> 1) * kD, tmem + (j & 1) * kBN + (kk >> 1) * 32 + (kk & 1) * 8,
-                               dv + s * (kKBytes >> 4) + kk * (2048 >> 4), id_o, j > 0 || (kk & 1));
-                tc_commit(&kv_empty[s]);
-                tc_commit(pv_done);
-                if (j == nb - 1) tc_commit(o_full);
-            }
-            __syncwarp();
-        }
-        if (!ok && lane == 0) {  // wind-down: wait for the MMAs already issued
-            volatile int never = 0;
-            tc_commit(drain);
-            mbar_wait(drain, 0, &never, 200000000ull);
         }
     } else {
         // ------------------------------------------------------------ softmax
+        regs_inc<kRegsSoftmax>();
+        // this thread's row of a tile and its half of the keys
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const int r_tok = r / G, r_head = r % G;
+        const bool row_used = r < TQ * G;
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tO = t_lane + kTmemO + half * kD;
-        const int i = r < TQ * G && tok < t.n ? first + tok : -1;
         const float sc = a.scale * kLog2e;
-        // blocks that every row sees whole begin in [full_lo, full_hi]
-        const int full_lo = i1 - a.w, full_hi = imin(i0 + 1, n_keys) - kBN;
-        float m = -INFINITY, l = 0.0f;
         bool ok = true;
-        for (int j = 0; j < nb; ++j) {
-            const int s = j % kStages, c0 = key_block(kb, b0 + j) * kBN;
-            const uint32_t tS = t_lane + (j & 1) * kBN + half * 32;
-            bool full = c0 <= full_hi && c0 >= full_lo;
-            ok = warp_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            float x[32];
-            tmem_ld32f(tS, x);
-            unsigned long long have = ~0ull;  // keys that exist (and, paged, that some row sees)
-            if constexpr (kPaged) {
-                // (published before the loads of the stage were issued)
-                ok = warp_wait(&k_full[s], (j / kStages) & 1, abort_flag);
+        int g = 0, it = 0;
+        for (int k = 0; ok; ++k) {
+            const Plan* p = next_plan(k);
+            if (!p || p->nb < 0) break;
+            const int nb = p->nb, n_keys = p->n_keys, tok = p->t0 + r_tok;
+            const bool row_stored = row_used && tok < p->rows;
+            const int i = row_used && tok < p->n ? p->first + tok : -1;  // this row's position
+            if (nb == 0) {
+                if (half == 0 && row_stored) {
+                    const size_t orow = ((size_t)p->batch * L + p->start + tok) * a.Hq + p->hk * G + r_head;
+                    zero_row64(static_cast<T*>(a.out) + orow * kD);
+                    if constexpr (!kPaged)
+                        a.lse[((size_t)p->batch * a.Hq + p->hk * G + r_head) * L + p->start + tok] = -INFINITY;
+                }
+                continue;
+            }
+            // blocks that every row sees whole begin in [full_lo, full_hi]
+            const int full_lo = p->i1 - a.w, full_hi = imin(p->i0 + 1, n_keys) - kBN;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nb; ++j) {
+                const int c = g + j, s = c % kStages, c0 = p->key0(j);
+                const uint32_t tS = t_lane + (c & 1) * kBN + half * 32;
+                bool full = c0 <= full_hi && c0 >= full_lo;
+                ok = warp_wait(&s_full[c & 1], (c >> 1) & 1, abort_flag);
                 if (!ok) break;
-                have = valid[s];
-                full = full && have == ~0ull;
-            } else if (c0 + kBN > n_keys) {
-                have = low_bits64(n_keys - c0);
-            }
-            tmem_ld_wait();
-            regs_ready<32>(x);
-            if (!full) {
-                const uint32_t bits = visible_bits32(i, c0 + half * 32, n_keys, a.w, a.sinks) & (uint32_t)(have >> (32 * half));
-#pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1 ? x[c] : -INFINITY;
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-                mx[0] = max3(mx[0], x[c], x[c + 1]);
-                mx[1] = max3(mx[1], x[c + 2], x[c + 3]);
-                mx[2] = max3(mx[2], x[c + 4], x[c + 5]);
-                mx[3] = max3(mx[3], x[c + 6], x[c + 7]);
-            }
-            const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-            const bool need = cm > m + kRescale || (m == -INFINITY && cm > m);
-            if (__any_sync(0xffffffffu, need)) {
-                const bool real = need && m != -INFINITY;
-                if (__any_sync(0xffffffffu, real)) {
-                    // every earlier product into O must be done (PV_(j-2) and
-                    // before are, since S_j is)
-                    ok = warp_wait(pv_done, (j - 1) & 1, abort_flag);
+                tc_fence_after();
+                float x[32];
+                tmem_ld32f(tS, x);
+                unsigned long long have = ~0ull;  // keys that exist (and, paged, that some row sees)
+                if constexpr (kPaged) {
+                    // (published before the loads of the stage were issued)
+                    ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
                     if (!ok) break;
-                    tc_fence_after();
-                    const float f = real ? ex2(m - cm) : 1.0f;
-                    l *= f;
+                    have = valid[s];
+                    full = full && have == ~0ull;
+                } else if (c0 + kBN > n_keys) {
+                    have = low_bits64(n_keys - c0);
+                }
+                tmem_ld_wait();
+                regs_ready<32>(x);
+                if (!full) {
+                    const uint32_t bits =
+                        visible_bits32(i, c0 + half * 32, n_keys, a.w, a.sinks) & (uint32_t)(have >> (32 * half));
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        float o[16];
-                        tmem_ld16f(tO + h * 16, o);
-                        tmem_ld_wait();
-                        regs_ready<16>(o);
+                    for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? x[e] : -INFINITY;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) o[c] *= f;
-                        tmem_st16f(tO + h * 16, o);
+                for (int e = 0; e < 32; e += 8) {
+                    mx[0] = max3(mx[0], x[e], x[e + 1]);
+                    mx[1] = max3(mx[1], x[e + 2], x[e + 3]);
+                    mx[2] = max3(mx[2], x[e + 4], x[e + 5]);
+                    mx[3] = max3(mx[3], x[e + 6], x[e + 7]);
+                }
+                const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                const bool need = cm > m + kRescale || (m == -INFINITY && cm > m);
+                if (__any_sync(0xffffffffu, need)) {
+                    const bool real = need && m != -INFINITY;
+                    if (__any_sync(0xffffffffu, real)) {
+                        // the products into O must be done: the last one
+                        // releases its stage (and none follows without this
+                        // warp's P)
+                        ok = warp_wait(&kv_empty[(c - 1) % kStages], ((c - 1) / kStages) & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float f = real ? ex2(m - cm) : 1.0f;
+                        l *= f;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            float o[16];
+                            tmem_ld16f(tO + h * 16, o);
+                            tmem_ld_wait();
+                            regs_ready<16>(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16f(tO + h * 16, o);
+                        }
+                    }
+                    if (need) m = cm;
+                }
+                const float nm = m == -INFINITY ? 0.0f : -m;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float e0 = ex2(fmaf(x[2 * e], sc, nm)), e1 = ex2(fmaf(x[2 * e + 1], sc, nm));
+                    sum[(2 * e) & 3] += e0;
+                    sum[(2 * e + 1) & 3] += e1;
+                    pk[e] = Pair<T>::pack(e0, e1);
+                }
+                tmem_st16(tS, pk);
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (have != ~0ull) {
+                    // rows of V that are no key of the sequence: 0 * NaN is NaN
+                    ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
+                    if (!ok) break;
+                    const int row = threadIdx.x >> 2;
+                    if (!((have >> row) & 1)) {
+                        uint4* zr = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 3) * 32);
+                        zr[0] = zr[1] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[c & 1]);
+            }
+            if (ok) ok = warp_wait(o_full, it & 1, abort_flag);
+            if (ok) {  // join the halves
+                ml[half * kBM + r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                ok = warp_wait(ml_full, it & 1, abort_flag);
+            }
+            if (ok) {
+                tc_fence_after();
+                const float2 u0 = ml[r], u1 = ml[kBM + r];
+                const float top = fmaxf(u0.x, u1.x), base = top == -INFINITY ? 0.0f : top;
+                const float f0 = ex2(u0.x - base), f1 = ex2(u1.x - base);
+                const float sum = i >= 0 ? u0.y * f0 + u1.y * f1 : 0.0f;  // i < 0: no token of the sequence
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
+                const size_t orow = ((size_t)p->batch * L + p->start + tok) * a.Hq + p->hk * G + r_head;
+                float o[32], o1[32];
+                tmem_ld32f(t_lane + kTmemO + half * 32, o);
+                tmem_ld32f(t_lane + kTmemO + kD + half * 32, o1);
+                tmem_ld_wait();
+                regs_ready<32>(o);
+                regs_ready<32>(o1);
+                tc_fence_before();
+                // (a half that saw no key holds exact zeros)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = sum == 0.0f ? 0.0f : o[e] * f0 + o1[e] * f1;
+                if (row_stored) {
+                    if (kPaged && p->part) {
+                        const size_t at = (size_t)p->z * ((size_t)L * a.Hq) + orow;
+                        float4* d = reinterpret_cast<float4*>(pp.o + at * kD + half * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            d[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+                        if (half == 0) pp.lse[at] = lse2;
+                    } else {
+                        store_row32(static_cast<T*>(a.out) + orow * kD + half * 32, o, inv);
+                        if constexpr (!kPaged) {
+                            if (half == 0)
+                                a.lse[((size_t)p->batch * a.Hq + p->hk * G + r_head) * L + p->start + tok] = lse2 * kLn2;
+                        }
                     }
                 }
-                if (need) m = cm;
+                __syncwarp();
             }
-            const float nm = m == -INFINITY ? 0.0f : -m;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t pk[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float e0 = ex2(fmaf(x[2 * c], sc, nm)), e1 = ex2(fmaf(x[2 * c + 1], sc, nm));
-                sum[(2 * c) & 3] += e0;
-                sum[(2 * c + 1) & 3] += e1;
-                pk[c] = Pair<T>::pack(e0, e1);
-            }
-            tmem_st16(tS, pk);
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (have != ~0ull) {
-                // rows of V that are no key of the sequence: 0 * NaN is NaN
-                ok = warp_wait(&v_full[s], (j / kStages) & 1, abort_flag);
-                if (!ok) break;
-                const int row = threadIdx.x >> 2;
-                if (!((have >> row) & 1)) {
-                    uint4* z = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 3) * 32);
-                    z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[j & 1]);
-        }
-        if (ok) ok = warp_wait(o_full, 0, abort_flag);
-        // join the halves (an abort is seen by all eight warps or comes too
-        // late to matter: the barrier below is reached either way)
-        ml[half * kBM + r] = make_float2(m, l);
-        named_bar_sync(1, kSoftmaxWarps * 32);
-        if (ok) {
-            tc_fence_after();
-            const float2 u0 = ml[r], u1 = ml[kBM + r];
-            const float top = fmaxf(u0.x, u1.x), base = top == -INFINITY ? 0.0f : top;
-            const float f0 = ex2(u0.x - base), f1 = ex2(u1.x - base);
-            const float sum = i >= 0 ? u0.y * f0 + u1.y * f1 : 0.0f;  // i < 0: no token of the sequence
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
-            const size_t at = part ? (size_t)blockIdx.z * ((size_t)L * a.Hq) + orow : 0;
-            float o[32], o1[32];
-            tmem_ld32f(t_lane + kTmemO + half * 32, o);
-            tmem_ld32f(t_lane + kTmemO + kD + half * 32, o1);
-            tmem_ld_wait();
-            regs_ready<32>(o);
-            regs_ready<32>(o1);
-            // (a half that saw no key holds exact zeros)
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = sum == 0.0f ? 0.0f : o[c] * f0 + o1[c] * f1;
-            if (row_stored) {
-                if (part) {
-                    float4* d = reinterpret_cast<float4*>(pl.o + at * kD + half * 32);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        d[c] = make_float4(o[4 * c] * inv, o[4 * c + 1] * inv, o[4 * c + 2] * inv, o[4 * c + 3] * inv);
-                    if (half == 0) pl.lse[at] = lse2;
-                } else {
-                    store_row32(static_cast<T*>(a.out) + orow * kD + half * 32, o, inv);
-                    if constexpr (!kPaged) {
-                        if (half == 0) a.lse[((size_t)t.batch * a.Hq + head) * L + t.start + tok] = lse2 * kLn2;
-                    }
-                }
-            }
+            g += nb;
+            ++it;
         }
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) record_status(a.status, 0, LF_ERR_DEVICE_TIMEOUT);
-    if (warp == kSoftmaxWarps + 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
 }
 
 template <typename T, bool kPaged, typename A>
-lf_status launch(const Maps& maps, const A& a, const PagedPlan& pl, dim3 grid, cudaStream_t stream) {
+lf_status launch(const Maps& maps, const A& a, const PagedPlan& pp, long long items, cudaStream_t stream) {
     static std::atomic<bool> attr[64];  // the shared-memory opt-in, per device
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return LF_ERR_CUDA;
-    if (!attr[dev].load()) {
+    lf_status st;
+    DeviceCtx* d = current_device(&st);
+    if (!d) return st;
+    if (!attr[d->ordinal].load()) {
         if (cudaFuncSetAttribute(window_kernel<T, kPaged, A>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmemBytes) != cudaSuccess)
             return LF_ERR_CUDA;
-        attr[dev].store(true);
+        attr[d->ordinal].store(true);
     }
-    return launch_pdl(window_kernel<T, kPaged, A>, grid, dim3(kThreads), kSmemBytes, stream, maps, a, pl);
+    if (items > INT32_MAX / 2) return LF_ERR_TOO_LARGE;
+    const int grid = (int)(items < kCtas * d->sm_count ? items : kCtas * d->sm_count);
+    return launch_pdl(window_kernel<T, kPaged, A>, dim3(grid), dim3(kThreads), kSmemBytes, stream, maps, a, pp,
+                      (int)items);
 }
 
 }  // namespace
@@ -462,22 +591,22 @@ lf_status launch_window_forward_tc(const WindowArgs& a, cudaStream_t stream) {
     if (!make_heads_map(&maps.q, a.q, a.Hq, a.L, B, G, TQ) || !make_heads_map(&maps.k, a.k, a.Hkv, a.L, B, 1, kBN) ||
         !make_heads_map(&maps.v, a.v, a.Hkv, a.L, B, 1, kBN))
         return LF_ERR_CUDA;
-    const dim3 grid(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv);
-    const PagedPlan pl = {};
-    if (a.dtype == LF_F16) return launch<__half, false>(maps, a, pl, grid, stream);
-    return launch<__nv_bfloat16, false>(maps, a, pl, grid, stream);
+    const PagedPlan pp = {};
+    const long long items = (long long)token_slots(a.packed(), a.n_seqs, a.L, TQ) * a.Hkv;
+    if (a.dtype == LF_F16) return launch<__half, false>(maps, a, pp, items, stream);
+    return launch<__nv_bfloat16, false>(maps, a, pp, items, stream);
 }
 
-lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& pl, cudaStream_t stream) {
+lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& pp, cudaStream_t stream) {
     const int G = a.heads_group(), TQ = kBM / G, page = 1 << a.page_shift;
     Maps maps;
     if (!make_heads_map(&maps.q, a.q, a.Hq, a.T, 1, G, TQ) ||
         !make_heads_map(&maps.k, a.k, a.Hkv, page, a.num_pages, 1, imin(page, kBN)) ||
         !make_heads_map(&maps.v, a.v, a.Hkv, page, a.num_pages, 1, imin(page, kBN)))
         return LF_ERR_CUDA;
-    const dim3 grid(packed_slots(a.T, a.n_seqs, TQ), a.Hkv, pl.tensor_splits);
-    if (a.dtype == LF_F16) return launch<__half, true>(maps, a, pl, grid, stream);
-    return launch<__nv_bfloat16, true>(maps, a, pl, grid, stream);
+    const long long items = (long long)packed_slots(a.T, a.n_seqs, TQ) * a.Hkv * pp.tensor_splits;
+    if (a.dtype == LF_F16) return launch<__half, true>(maps, a, pp, items, stream);
+    return launch<__nv_bfloat16, true>(maps, a, pp, items, stream);
 }
 
 }  // namespace lf
