@@ -34,6 +34,14 @@ LF_HD KeyBlocks tile_key_blocks(int first, int t0, int t1, int kv, int w, int si
     return t0 < t1 && first + t1 - 1 >= 0 ? key_blocks(first + t0, first + t1 - 1, kv, w, sinks, 64) : k;
 }
 
+// Blocks of bk keys that up to max_q consecutive tokens see, at most: their
+// windows span w + max_q keys.
+inline long long most_blocks(int max_q, int width, int w, int sinks, int bk) {
+    const long long window = ((long long)w + max_q) / bk + 2 + (sinks + (long long)bk - 1) / bk;
+    const long long all = ((long long)width + bk - 1) / bk;
+    return window < all ? window : all;
+}
+
 // w and sinks clamped to the table's width.
 inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int width, int w, int sinks) {
     PagedPlan p = {};
@@ -41,29 +49,32 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
     p.tensor = (long long)max_q * G > kDecodeRows;
     // (with n_seqs * max_q tokens every sequence has max_q)
     p.decode = G <= kDecodeRows && !(p.tensor && (long long)n_seqs * max_q == T);
-    // Keys one sequence's tokens can see, at most.
-    const long long seen = width < (long long)w + max_q + sinks ? width : (long long)w + max_q + sinks;
     if (p.decode) {
         // About two rounds of CTAs (three of 4 warps fit an SM) over the
         // widest contexts, 128 to 1024 keys each: fewer, and a warp has no
         // second step to load under its first; more, and ragged contexts
         // leave SMs idle.
-        const long long tiles = seen / 8 + 2, all = tiles * n_seqs * Hkv;
+        const long long tiles = most_blocks(max_q, width, w, sinks, 8), all = tiles * n_seqs * Hkv;
         p.chunk = (int)(all / (2 * 3 * 148));
         p.chunk = iclamp((p.chunk + 15) / 16 * 16, 16, 128);
         if (tiles > 1024LL * p.chunk) p.chunk = (int)((tiles + 1023) / 1024);  // at most 1024 pieces
         p.decode_splits = (int)((tiles + p.chunk - 1) / p.chunk);
     }
     if (p.tensor) {
-        // Split only when the tiles leave most of the 4 x 148 CTA slots idle,
-        // into pieces of at least 8 blocks.
+        // Rounds of the 2 x 148 resident CTAs times blocks per item; pieces
+        // are joined by a further kernel, worth about 12 blocks.
         const long long tiles = (long long)packed_slots(T, n_seqs, 128 / G) * Hkv;
-        const long long blocks = seen / 64 + 2;
-        const long long want = (4 * 148) / tiles;
-        long long per = want > 1 ? (blocks + want - 1) / want : blocks;
-        if (per < 8) per = 8;
-        p.per = (int)per;
-        p.tensor_splits = (int)((blocks + per - 1) / per);
+        const long long blocks = most_blocks(max_q, width, w, sinks, 64);
+        long long best = -1;
+        for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
+            const long long per = (blocks + s - 1) / s, rounds = (tiles * s + 295) / 296;
+            const long long cost = rounds * (per + 2) + (s > 1 ? 12 : 0);
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.per = (int)per;
+                p.tensor_splits = (int)((blocks + per - 1) / per);
+            }
+        }
     }
     return p;
 }

@@ -481,17 +481,18 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     if (need) m = cm;
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float e0 = ex2(fmaf(x[2 * e], sc, nm)), e1 = ex2(fmaf(x[2 * e + 1], sc, nm));
-                    sum[(2 * e) & 3] += e0;
-                    sum[(2 * e + 1) & 3] += e1;
-                    pk[e] = Pair<T>::pack(e0, e1);
+                    const float2 v = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nm2);
+                    const float2 q = make_float2(ex2(v.x), ex2(v.y));
+                    sum[e & 1] = fadd2(sum[e & 1], q);
+                    pk[e] = Pair<T>::pack(q.x, q.y);
                 }
                 tmem_st16(tS, pk);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 if (have != ~0ull) {
                     // rows of V that are no key of the sequence: 0 * NaN is NaN
                     ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);

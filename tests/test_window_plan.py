@@ -12,7 +12,7 @@ import pytest
 from sparse_attention_banded_b200 import build
 
 SRC = r'''
-#include "lf_visible.h"
+#include "lf_paged_split.h"
 using namespace lf;
 extern "C" {
 int slots(int packed, int n, int L, int unit) { return token_slots(packed != 0, n, L, unit); }
@@ -30,6 +30,12 @@ int full(int i0, int i1, int j0, int bk, int nk, int w, int s) { return block_fu
 int range_vis(int i0, int i1, int j0, int j1, int w, int s) { return range_visible(i0, i1, j0, j1, w, s); }
 unsigned long long bits(int i, int c0, int nk, int w, int s) { return visible_bits(i, c0, nk, w, s); }
 unsigned bits32(int i, int c0, int nk, int w, int s) { return visible_bits32(i, c0, nk, w, s); }
+void plan(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int* o) {
+    PagedPlan p = paged_plan(n, Hq, Hkv, T, mq, width, w, s);
+    o[0] = p.decode; o[1] = p.tensor; o[2] = p.chunk; o[3] = p.decode_splits; o[4] = p.per; o[5] = p.tensor_splits;
+}
+int tiles8(int first, int n, int kv, int w, int s) { return decode_tiles(first, n, kv, w, s).n; }
+int blocks64(int first, int t0, int t1, int kv, int w, int s) { return tile_key_blocks(first, t0, t1, kv, w, s).n; }
 int page(const int* row, int mp, int np, int sh, int j) { return page_of(row, mp, np, sh, j); }
 }
 '''
@@ -137,3 +143,34 @@ def test_pages_outside_the_table_are_missing(P):
     row = _arr([3, -1, 7, 99, 0])
     assert [P.page(row, 5, 8, 4, j) for j in (0, 15, 16, 32, 48, 64, 79, 80, -1, 2 ** 31 - 1)] == \
         [3, 3, -1, 7, -1, 0, 0, -1, -1, -1]
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_a_plan_covers_every_context(P, seed):
+    """The pieces a call is cut into hold every block its sequences can see,
+    and every sequence belongs to a kernel that is launched."""
+    r = random.Random(seed)
+    Hkv = r.choice([1, 2, 5])
+    G = r.choice([1, 2, 3, 8, 17, 64])
+    n = r.randint(1, 20)
+    page = r.choice([8, 16, 64, 512])
+    width = page * r.randint(1, 400)
+    qs = [r.choice([0, 1, 1, r.randint(1, min(width, 300))]) for _ in range(n)]
+    mq = max(max(qs), 1)
+    T = max(sum(qs), 1)
+    w = min(width, r.choice([0, 1, 63, 64, 100, 1000, 1 << 20]))
+    s = min(width, r.choice([0, 1, 4, 64, 70]))
+    o = (ctypes.c_int * 6)()
+    P.plan(n, G * Hkv, Hkv, T, mq, width, w, s, o)
+    decode, tensor, chunk, splits8, per, splits64 = o
+    for q in qs:
+        if not q:
+            continue
+        kv = r.randint(q, width)
+        if decode and q * G <= 16:
+            assert P.tiles8(kv - q, q, kv, w, s) <= chunk * splits8
+        else:
+            assert tensor
+            TQ = 128 // G
+            for t0 in range(0, q, TQ):
+                assert P.blocks64(kv - q, t0, min(t0 + TQ, q), kv, w, s) <= per * splits64
