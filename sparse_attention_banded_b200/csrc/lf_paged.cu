@@ -3,7 +3,7 @@
 // Token t of sequence b's n_b new ones goes to position kv_lens[b] - n_b + t.
 // A copy, bound by HBM (and by its launch for a few tokens): 8 threads move
 // one 128-byte row of k and of v with 16-byte accesses.
-#include "lf_window.h"
+#include "lf_tc_tiles.cuh"
 
 namespace lf {
 namespace {
@@ -11,12 +11,17 @@ namespace {
 constexpr int kRowsPerBlock = 32;
 
 __global__ void __launch_bounds__(kRowsPerBlock * 8) append_kernel(const __grid_constant__ PagedArgs a) {
+    sm100::pdl_launch_dependents();
+    sm100::pdl_wait();
     const int part = threadIdx.x & 7;
     const long long row = (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 3);  // (token, kv head)
     if (blockIdx.x == 0) check_lengths(a.cu, nullptr, a.n_seqs, a.T, a.status, threadIdx.x, blockDim.x);
+    const int tok = imin((int)(row / a.Hkv), a.T - 1), h = (int)(row % a.Hkv);
+    // a warp holds four rows, of tokens in order: the first one's sequence
+    // is the others' too, or they search on from it
+    int b = seq_of_token_warp(a.cu, a.n_seqs, __shfl_sync(0xffffffffu, tok, 0));
+    while (b + 1 < a.n_seqs && a.cu[b + 1] <= tok) ++b;
     if (row >= (long long)a.T * a.Hkv) return;
-    const int tok = (int)(row / a.Hkv), h = (int)(row % a.Hkv);
-    const int b = seq_of_token(a.cu, a.n_seqs, tok);
     if (tok < a.cu[b] || tok >= a.cu[b + 1]) return;  // behind the last sequence
     const int j = a.kv_lens[b] - (a.cu[b + 1] - tok);
     const int page = page_of(a.table + (size_t)b * a.max_pages, a.max_pages, a.num_pages, a.page_shift, j);
@@ -38,8 +43,8 @@ __global__ void __launch_bounds__(kRowsPerBlock * 8) append_kernel(const __grid_
 
 lf_status launch_paged_append(const PagedArgs& a, cudaStream_t stream) {
     const long long rows = (long long)a.T * a.Hkv;
-    append_kernel<<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), kRowsPerBlock * 8, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
+    return launch_pdl(append_kernel, dim3((unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock)),
+                      dim3(kRowsPerBlock * 8), 0, stream, a);
 }
 
 }  // namespace lf

@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= (long long)a.T * a.Hq) return;
     const int tok = (int)(row / a.Hq), G = a.Hq / a.Hkv;
-    const int b = seq_of_token(a.cu, a.n_seqs, tok);
+    const int b = seq_of_token_warp(a.cu, a.n_seqs, tok);
     const int start = iclamp(a.cu[b], 0, a.T), n = iclamp(a.cu[b + 1], 0, a.T) - start;
     if (tok < start || tok >= start + n) return;
     int kv, first;

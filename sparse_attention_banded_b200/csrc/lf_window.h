@@ -77,6 +77,21 @@ __device__ __forceinline__ bool paged_seq(const PagedArgs& a, int b, int n, int&
     return n <= a.max_q;
 }
 
+// The last sequence that starts at or before the token, by a whole warp: 32
+// offsets at a time (one memory latency for up to 32 sequences, where a
+// binary search takes five).
+__device__ __forceinline__ int seq_of_token_warp(const int32_t* cu, int n_seqs, int token) {
+    if (n_seqs > 512) return seq_of_token(cu, n_seqs, token);
+    int count = 0;
+    for (int b = 0; b < n_seqs; b += 32) {
+        const int i = b + (threadIdx.x & 31);
+        const unsigned before = __ballot_sync(0xffffffffu, i < n_seqs && cu[i] <= token);
+        count += __popc(before);
+        if (before != 0xffffffffu) break;
+    }
+    return imax(count - 1, 0);
+}
+
 // The offsets must ascend from 0 to at most L, and lengths fit; records the
 // sequences whose do not (every access is clamped anyway).  Called by one
 // group of `step` threads.
