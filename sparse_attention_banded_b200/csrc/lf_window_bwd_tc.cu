@@ -19,7 +19,10 @@
 // The 8 math warps split a tile's columns in halves (two threads a row), the
 // 16-bit P or dS of a half overwriting the first 16 columns of that half's
 // scores.  256 tensor-memory columns a CTA, two CTAs per SM: one's products
-// run under the other's exponentials.  P and dS are rounded to the storage
+// run under the other's arithmetic, which is what bounds both kernels (a
+// third of the exponentials on the FMA pipe, 13 instructions a pair, and
+// selects in tiles without a mask cost 712 us where 578 us are left at 16384
+// packed tokens, 16 / 4 heads, window 1024, forward and backward).  P and dS are rounded to the storage
 // type, the MMA's operand type; accumulators are fp32, rounded once.
 //
 // Rows of other sequences (or of no token) that a tile's loads bring along
@@ -48,7 +51,7 @@ constexpr uint32_t kOffB = 2 * kBig;                       // moving: stage s, t
 constexpr uint32_t kOffRow = kOffB + kStages * 2 * kSmall; // floats
 constexpr uint32_t kRowFloats = kStages * 128;
 constexpr uint32_t kOffBar = kOffRow + kRowFloats * 4;
-constexpr uint32_t kBars = 1 + 2 * kStages + 6;
+constexpr uint32_t kBars = 1 + 2 * kStages + 7;
 constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;      // + alignment slack
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -59,7 +62,7 @@ struct Maps {
 
 struct Ctx {
     uint8_t* smem;
-    uint64_t *a_full, *b_full, *b_empty, *s_full, *free_, *ready, *done, *drain;
+    uint64_t *a_full, *b_full, *b_empty, *s_full, *dp_full, *free_, *ready, *done, *drain;
     volatile int* abort_flag;
     uint32_t tmem;
 };
@@ -72,7 +75,8 @@ __device__ __forceinline__ Ctx setup(uint8_t* smem, int warp, int lane) {
     c.b_full = c.a_full + 1;
     c.b_empty = c.b_full + kStages;
     c.s_full = c.b_empty + kStages;
-    c.free_ = c.s_full + 1;
+    c.dp_full = c.s_full + 1;
+    c.free_ = c.dp_full + 1;
     c.ready = c.free_ + 1;  // [2]
     c.done = c.ready + 2;
     c.drain = c.done + 1;
@@ -85,6 +89,7 @@ __device__ __forceinline__ Ctx setup(uint8_t* smem, int warp, int lane) {
             mbar_init(&c.b_empty[s], 1);
         }
         mbar_init(c.s_full, 1);
+        mbar_init(c.dp_full, 1);
         mbar_init(c.free_, kMathWarps);
         mbar_init(&c.ready[0], kMathWarps);
         mbar_init(&c.ready[1], kMathWarps);
@@ -137,11 +142,6 @@ __device__ __forceinline__ void mma_nt(uint32_t d, uint32_t a_smem, uint32_t b_s
 template <typename T>
 __device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a_tmem, uint32_t b_smem, bool accumulate) {
     mma4_ts(d, d, a_tmem, desc_sw128(b_smem, 0), idesc_f16(MmaFormat<T>::fmt, 128, 64, 0, 1), accumulate, 1);
-}
-
-// exp2 of a pair; in a tile without masked scores a third run on the FMA pipe.
-__device__ __forceinline__ float2 exp_pair(float2 v, bool poly) {
-    return poly ? exp2_poly2(v) : make_float2(ex2(v.x), ex2(v.y));
 }
 
 // Zero the rows [from, 64) of a 64-row tile (256 math threads).
@@ -267,12 +267,14 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const float sc = a.scale * kLog2e;
         const float2 sc2 = make_float2(sc, sc), nl2 = make_float2(nlse, nlse), nd2 = make_float2(ndelta, ndelta);
+        // blocks that every row of this warp sees whole begin in [full_lo, full_hi]
+        const bool warp_live = __all_sync(0xffffffffu, live);
+        const int full_lo = i1 - a.w, full_hi = imin(i0 + 1, t.n) - 64;
         bool ok = true;
         for (int j = 0; j < kb.n; ++j) {
             const int c0 = key_block(kb, j) * 64;
             const uint32_t tS = tmS + lane_off + (j & 1) * 64 + half * 32;
-            const uint32_t bits = live ? (uint32_t)(visible_bits(tok, c0, t.n, a.w, a.sinks) >> (32 * half)) : 0u;
-            const bool full = __all_sync(0xffffffffu, bits == ~0u);
+            const bool full = warp_live && c0 <= full_hi && c0 >= full_lo;
             ok = warp_wait(c.s_full, j & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -286,15 +288,21 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
             __syncwarp();
             if (lane == 0) mbar_arrive(c.free_);
             uint32_t pk[16];
+            if (full) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 p = exp_pair(ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nl2), full && e % 3 == 2);
-                float2 d = fmul2(p, fadd2(make_float2(y[2 * e], y[2 * e + 1]), nd2));
-                if (!full) {
-                    d.x = (bits >> (2 * e)) & 1 ? d.x : 0.0f;
-                    d.y = (bits >> (2 * e + 1)) & 1 ? d.y : 0.0f;
+                for (int e = 0; e < 16; ++e) {
+                    const float2 v = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nl2);
+                    const float2 d = fmul2(make_float2(ex2(v.x), ex2(v.y)), fadd2(make_float2(y[2 * e], y[2 * e + 1]), nd2));
+                    pk[e] = Pair<T>::pack(d.x, d.y);
                 }
-                pk[e] = Pair<T>::pack(d.x, d.y);
+            } else {
+                const uint32_t bits = live ? visible_bits32(tok, c0 + 32 * half, t.n, a.w, a.sinks) : 0u;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 v = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nl2);
+                    const float2 d = fmul2(make_float2(ex2(v.x), ex2(v.y)), fadd2(make_float2(y[2 * e], y[2 * e + 1]), nd2));
+                    pk[e] = Pair<T>::pack((bits >> (2 * e)) & 1 ? d.x : 0.0f, (bits >> (2 * e + 1)) & 1 ? d.y : 0.0f);
+                }
             }
             tmem_st16(tS, pk);
             if (c0 + 64 > t.n) {  // keys past the sequence
@@ -345,29 +353,34 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
     const int nq = q1 > q0 ? (q1 - q0 + TQ - 1) / TQ : 0;
 
     const int r = (warp & 3) * 32 + lane, half = warp >> 2, key = c0 + r;
-    // where this thread's half rows of dK and dV go: the fp32 partials of a
-    // sink key, or the outputs
-    const int n_sink = imin(a.sinks, t.n);
-    float* part = nullptr;
-    T *dk = nullptr, *dv = nullptr;
-    if (warp < kMathWarps) {
-        if (key < n_sink) {
-            part = a.part + (((size_t)(sink ? a.n_seqs + slot : t.b) * a.Hkv + hk) * a.sinks + key) * 2 * kD + half * 32;
+    // Where this thread's half rows of dK and dV go: the fp32 partials of a
+    // sink key, or the outputs (worked out when they are needed).
+    struct Target {
+        float* part;
+        T *dk, *dv;
+    };
+    auto target = [&]() -> Target {
+        Target o = {nullptr, nullptr, nullptr};
+        if (warp >= kMathWarps) return o;
+        if (key < imin(a.sinks, t.n)) {
+            o.part = a.part + (((size_t)(sink ? a.n_seqs + slot : t.b) * a.Hkv + hk) * a.sinks + key) * 2 * kD + half * 32;
         } else if (!sink && key < t.rows) {
-            dk = view_row<T>(a.dk, t.batch, hk, t.start + key) + half * 32;
-            dv = view_row<T>(a.dv, t.batch, hk, t.start + key) + half * 32;
+            o.dk = view_row<T>(a.dk, t.batch, hk, t.start + key) + half * 32;
+            o.dv = view_row<T>(a.dv, t.batch, hk, t.start + key) + half * 32;
         }
-    }
+        return o;
+    };
     if (nq == 0) {  // padding, or a chunk inside every window
-        if (part) {
+        const Target o = target();
+        if (o.part) {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                reinterpret_cast<float4*>(part)[u] = reinterpret_cast<float4*>(part + kD)[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                reinterpret_cast<float4*>(o.part)[u] = reinterpret_cast<float4*>(o.part + kD)[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (dk) {
+        if (o.dk) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                reinterpret_cast<uint4*>(dk)[u] = reinterpret_cast<uint4*>(dv)[u] = make_uint4(0u, 0u, 0u, 0u);
+                reinterpret_cast<uint4*>(o.dk)[u] = reinterpret_cast<uint4*>(o.dv)[u] = make_uint4(0u, 0u, 0u, 0u);
         }
         return;
     }
@@ -419,22 +432,40 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
         if (!ok && lane == 0) drain_loads(c, j);
     } else if (warp == kMathWarps + 1) {
         // ------------------------------------------------------------ MMA
+        // In issue order S_0, dP_0, then per tile dV_j, S_(j+1) once P is
+        // there and dK_j, dP_(j+1) once dS is: S_(j+1) may overwrite P_j, and
+        // dP_(j+1) dS_j, without a wait, and each pair runs under the other
+        // half of the math warps' step.
         const uint32_t b0 = smem_u32(smem + kOffB);
-        bool ok = warp_wait(c.a_full, 0, c.abort_flag);
-        for (int j = 0; j < nq && ok; ++j) {
-            const int s = j % kStages;
-            const uint32_t bq = b0 + s * 2 * kSmall, bo = bq + kSmall;
-            ok = warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag);
-            if (!ok) break;
+        bool ok = warp_wait(c.a_full, 0, c.abort_flag) && warp_wait(&c.b_full[0], 0, c.abort_flag);
+        if (ok) {
             tc_fence_after();
-            mma_nt<T>(tmS, smem_u32(smem), bq);
-            mma_nt<T>(tmP, smem_u32(smem + kBig), bo);
+            mma_nt<T>(tmS, smem_u32(smem), b0);
             commit_elect(c.s_full);
-            ok = warp_wait(&c.ready[0], j & 1, c.abort_flag);
+            mma_nt<T>(tmP, smem_u32(smem + kBig), b0 + kSmall);
+            commit_elect(c.dp_full);
+        }
+        for (int j = 0; j < nq && ok; ++j) {
+            const int s = j % kStages, s1 = (j + 1) % kStages;
+            const uint32_t bq = b0 + s * 2 * kSmall, bq1 = b0 + s1 * 2 * kSmall;
+            const bool more = j + 1 < nq;
+            ok = (!more || warp_wait(&c.b_full[s1], ((j + 1) / kStages) & 1, c.abort_flag)) &&
+                 warp_wait(&c.ready[0], j & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
-            mma_tn<T>(tmV, tmS, bo, j > 0);
+            mma_tn<T>(tmV, tmS, bq + kSmall, j > 0);
+            if (more) {
+                mma_nt<T>(tmS, smem_u32(smem), bq1);
+                commit_elect(c.s_full);
+            }
+            ok = warp_wait(&c.ready[1], j & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
             mma_tn<T>(tmK, tmP, bq, j > 0);
+            if (more) {
+                mma_nt<T>(tmP, smem_u32(smem + kBig), bq1 + kSmall);
+                commit_elect(c.dp_full);
+            }
             commit_elect(&c.b_empty[s]);
             if (j == nq - 1) commit_elect(c.done);
         }
@@ -450,48 +481,42 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
             const int s = j % kStages, qt = q0 + j * TQ;
             // columns (query rows) that see this thread's key: tokens from
             // the key on to the window's end, or past it for a sink
-            unsigned long long vis = 0;
-            if (key < n_keys) {
-                const int past = iclamp(key + a.w + 1 - qt, 0, 64) * G;
-                vis = low_bits64(iclamp(q1 - qt, 0, TQ) * G);
-                vis &= sink ? ~low_bits64(past) : low_bits64(past) & ~low_bits64(iclamp(key - qt, 0, 64) * G);
-            }
-            const uint32_t bits = (uint32_t)(vis >> (32 * half));
+            const int past = iclamp(key + a.w + 1 - qt, 0, 64) * G, end = imin(q1 - qt, TQ) * G;
+            const int lo = sink ? past : iclamp(key - qt, 0, 64) * G, hi = sink ? end : imin(past, end);
+            const uint32_t bits = key < n_keys ? low_bits32(hi - 32 * half) & ~low_bits32(lo - 32 * half) : 0u;
             const bool full = __all_sync(0xffffffffu, bits == ~0u);
+            const float4* nl4 = reinterpret_cast<const float4*>(row_s + s * 128 + half * 32);
+            const float4* nd4 = nl4 + 16;
             ok = warp_wait(c.s_full, j & 1, c.abort_flag) && warp_wait(&c.b_full[s], (j / kStages) & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
-            float x[32], y[32];
+            // P, kept in fp32 for dS
+            float x[32];
+            uint32_t pk[16];
             tmem_ld32f(tS, x);
-            tmem_ld32f(tP, y);
-            const float4* nl4 = reinterpret_cast<const float4*>(row_s + s * 128 + half * 32);
-            const float4* nd4 = nl4 + 16;
             tmem_ld_wait();
             regs_ready<32>(x);
-            regs_ready<32>(y);
-            uint32_t pp[16], pd[16];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const float4 nl = nl4[u], nd = nd4[u];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int e = 2 * u + h;
-                    const float2 l2 = h ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
-                    const float2 d2 = h ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y);
-                    float2 p = exp_pair(ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, l2), full && e % 3 == 2);
-                    float2 d = fmul2(p, fadd2(make_float2(y[2 * e], y[2 * e + 1]), d2));
-                    if (!full) {
-                        const bool b0 = (bits >> (2 * e)) & 1, b1 = (bits >> (2 * e + 1)) & 1;
-                        p = make_float2(b0 ? p.x : 0.0f, b1 ? p.y : 0.0f);
-                        d = make_float2(b0 ? d.x : 0.0f, b1 ? d.y : 0.0f);
-                    }
-                    pp[e] = Pair<T>::pack(p.x, p.y);
-                    pd[e] = Pair<T>::pack(d.x, d.y);
-                }
+                const float4 nl = nl4[u];
+                const float2 v0 = ffma2(make_float2(x[4 * u], x[4 * u + 1]), sc2, make_float2(nl.x, nl.y));
+                const float2 v1 = ffma2(make_float2(x[4 * u + 2], x[4 * u + 3]), sc2, make_float2(nl.z, nl.w));
+                x[4 * u] = ex2(v0.x);
+                x[4 * u + 1] = ex2(v0.y);
+                x[4 * u + 2] = ex2(v1.x);
+                x[4 * u + 3] = ex2(v1.y);
             }
-            tmem_st16(tS, pp);
-            tmem_st16(tP, pd);
+            if (!full) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? x[e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = Pair<T>::pack(x[2 * e], x[2 * e + 1]);
+            tmem_st16(tS, pk);
             if (qt + TQ > t.n) {  // query rows past the sequence
+                // (dP reads dO: only what is of no use to it changes, but not under it)
+                ok = warp_wait(c.dp_full, j & 1, c.abort_flag);
+                if (!ok) break;
                 uint8_t* d = smem + kOffB + s * 2 * kSmall;
                 zero_rows(d, (t.n - qt) * G);
                 zero_rows(d + kSmall, (t.n - qt) * G);
@@ -501,9 +526,39 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.ready[0]);
+            // dS
+            ok = warp_wait(c.dp_full, j & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            float y[32];
+            tmem_ld32f(tP, y);
+            tmem_ld_wait();
+            regs_ready<32>(y);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float4 nd = nd4[u];
+                const float2 d0 = fmul2(make_float2(x[4 * u], x[4 * u + 1]), fadd2(make_float2(y[4 * u], y[4 * u + 1]), make_float2(nd.x, nd.y)));
+                const float2 d1 = fmul2(make_float2(x[4 * u + 2], x[4 * u + 3]), fadd2(make_float2(y[4 * u + 2], y[4 * u + 3]), make_float2(nd.z, nd.w)));
+                y[4 * u] = d0.x;
+                y[4 * u + 1] = d0.y;
+                y[4 * u + 2] = d1.x;
+                y[4 * u + 3] = d1.y;
+            }
+            if (!full) {  // (0 times what a dead row's dP holds)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = (bits >> e) & 1 ? y[e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = Pair<T>::pack(y[2 * e], y[2 * e + 1]);
+            tmem_st16(tP, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.ready[1]);
         }
         if (ok && warp_wait(c.done, 0, c.abort_flag)) {
             tc_fence_after();
+            const Target to = target();
 #pragma unroll
             for (int w = 0; w < 2; ++w) {  // dK, dV
                 float o[32];
@@ -511,15 +566,14 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
                 tmem_ld_wait();
                 regs_ready<32>(o);
                 const float f = w ? 1.0f : a.scale;
-                const bool live = key < n_keys;
-                if (part) {
-                    float4* d = reinterpret_cast<float4*>(part + w * kD);
+                if (to.part) {
+                    float4* d = reinterpret_cast<float4*>(to.part + w * kD);
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
                         d[u] = make_float4(o[4 * u] * f, o[4 * u + 1] * f, o[4 * u + 2] * f, o[4 * u + 3] * f);
-                } else if (dk) {
-                    T* d = w ? dv : dk;
-                    if (live) store_row32(d, o, f);
+                } else if (to.dk) {
+                    T* d = w ? to.dv : to.dk;
+                    if (key < n_keys) store_row32(d, o, f);
                     else
 #pragma unroll
                         for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(d)[u] = make_uint4(0u, 0u, 0u, 0u);

@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(128) sink_reduce_kernel(const __grid_constant_
     float s = p[b * step];
     const int first = a.cu ? start / a.chunk + b : b * ((a.L + a.chunk - 1) / a.chunk);
     const int chunks = (n + a.chunk - 1) / a.chunk;
+#pragma unroll 16
     for (int c = 0; c < chunks; ++c) s += p[(size_t)(a.n_seqs + first + c) * step];
     const lf_heads& v = e < kD ? a.dk : a.dv;
     static_cast<T*>(v.data)[(a.cu ? 0 : b) * v.batch_stride + hk * v.head_stride + (start + key) * v.token_stride +
