@@ -565,7 +565,8 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
  *          elements apart (>= N)
  *   gamma, beta  [N] float32, or NULL (1, 0)
  *   y      [rows, N] of dtype, dense
- *   mean, rstd   [rows] float32, or NULL when no gradient is wanted
+ *   mean, rstd   [rows] float32 (4-byte aligned), or NULL when no gradient is
+ *          wanted
  * 1 <= N <= 16384 (LF_ERR_TOO_LARGE above), eps >= 0 and finite; rows = 0
  * does nothing.  Errors: LF_ERR_NULL, LF_ERR_BAD_DIM, LF_ERR_DTYPE,
  * LF_ERR_MISALIGNED (pointers; strides are free).  Asynchronous, no scratch.

@@ -273,8 +273,9 @@ lf_status lf_layer_norm_forward(const void* x, long long x_stride, const float* 
     lf_status st = check_norm(rows, N, x_stride, N, dtype);
     if (st != LF_OK) return st;
     if (!(eps >= 0.f) || !isfinite(eps)) return LF_ERR_BAD_DIM;
-    for (const void* p : {x, (const void*)gamma, (const void*)beta, (const void*)y, (const void*)mean, (const void*)rstd})
+    for (const void* p : {x, (const void*)gamma, (const void*)beta, (const void*)y})
         if (!aligned16(p)) return LF_ERR_MISALIGNED;
+    if (misaligned4(mean, rstd, nullptr)) return LF_ERR_MISALIGNED;
     if (rows == 0) return LF_OK;
     if (!current_device(&st)) return st;
     NormArgs a = {};
@@ -304,9 +305,9 @@ lf_status lf_layer_norm_backward(const void* dy, long long dy_stride, const void
     if (rows != 0 && (!dy || !x || !mean || !rstd || !dx)) return LF_ERR_NULL;
     lf_status st = check_norm(rows, N, x_stride, dy_stride, dtype);
     if (st != LF_OK) return st;
-    for (const void* p : {dy, x, (const void*)gamma, (const void*)mean, (const void*)rstd, (const void*)dx,
-                          (const void*)dgamma, (const void*)dbeta})
+    for (const void* p : {dy, x, (const void*)gamma, (const void*)dx, (const void*)dgamma, (const void*)dbeta})
         if (!aligned16(p)) return LF_ERR_MISALIGNED;
+    if (misaligned4(mean, rstd, nullptr)) return LF_ERR_MISALIGNED;
     const bool params = dgamma || dbeta;
     if (params && rows > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
                                workspace_bytes < norm_backward_bytes(rows, N)))

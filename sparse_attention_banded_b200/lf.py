@@ -430,56 +430,78 @@ def _dense(t):
 
 
 def _want(name, t, dtype=None, shape=None):
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
     if shape is not None and t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
 
 
+def _new(t, like, dtype, shape, name):
+    """`t` checked, or a new tensor on the device of `like`."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _want(name, t, dtype, shape)
+
+
+def _workspace(t, like, need):
+    """(tensor, address, bytes) of the caller's workspace or a new one."""
+    if t is None:
+        if not need:
+            return None, None, 0
+        t = like.new_empty(need, dtype=torch.uint8)
+        return t, t.data_ptr(), need
+    return t, _dense(t), t.numel() * t.element_size()
+
+
+_INT32 = range(-(1 << 31), 1 << 31)
+
+
 def _int32(**values):
     for name, x in values.items():
-        if not -(1 << 31) <= x < 1 << 31:
+        if x not in _INT32:
             raise ValueError("%s: %d is not an int32" % (name, x))
 
 
-def _heads(name, t, dtype=None, shape=None):
+def _heads(name, t, shape=None, dtype=None):
     """lf_heads of [B, H, T, 64], or of packed [T, H, 64]."""
-    _want(name, t, dtype, shape)
+    if dtype is not None:
+        _want(name, t, dtype, shape)
     strides = t.stride()
-    if t.dim() not in (3, 4) or t.shape[-1] != 64:
-        raise ValueError("%s: expected [B, H, L, 64] or packed [T, H, 64], got %s" % (name, tuple(t.shape)))
-    if strides[-1] != 1 and t.numel():
-        raise ValueError("%s: the last dimension must be contiguous" % name)
+    if t.shape[-1] != 64 or strides[-1] != 1 and t.numel():
+        raise ValueError("%s: expected rows of 64 contiguous elements, got %s" % (name, tuple(t.shape)))
     if len(strides) == 3:
         return Heads(t.data_ptr(), 0, strides[1], strides[0])
     return Heads(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
 def _window_shape(q, k, v, cu_seqlens, seq_lens):
-    """(packed, n_seqs, Hq, Hkv, L, shape of out, shape of lse)"""
+    """(n_seqs, Hq, Hkv, L, shape of out, shape of lse)"""
+    shape, dtype = q.shape, q.dtype
     packed = cu_seqlens is not None
-    if q.dim() != (3 if packed else 4):
-        raise ValueError("q: expected %s, got %s" % ("packed [T, H, 64]" if packed else "[B, H, L, 64]",
-                                                     tuple(q.shape)))
+    if len(shape) != (3 if packed else 4) or shape[-1] != 64:
+        raise ValueError("q: expected %s, got %s" % ("packed [T, H, 64]" if packed else "[B, H, L, 64]", tuple(shape)))
+    kv = k.shape
+    if k.dtype is not dtype or v.dtype is not dtype or v.shape != kv or len(kv) != len(shape):
+        raise ValueError("k, v: expected two [.., Hkv, .., 64] of %s like q, got %s and %s" % (dtype, tuple(kv), tuple(v.shape)))
     if packed:
-        _want("cu_seqlens", cu_seqlens, torch.int32)
+        L, Hq, _ = shape
+        Hkv = kv[1]
+        if kv != (L, Hkv, 64):
+            raise ValueError("k: expected (%d, Hkv, 64), got %s" % (L, tuple(kv)))
         if seq_lens is not None:
             raise ValueError("give cu_seqlens or seq_lens, not both")
-        L, Hq, _ = q.shape
-        Hkv = k.shape[1]
-        _want("k", k, q.dtype, (L, Hkv, 64))
-        _want("v", v, q.dtype, (L, Hkv, 64))
+        _want("cu_seqlens", cu_seqlens, torch.int32)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens: expected [n_seqs + 1]")
-        return True, cu_seqlens.numel() - 1, Hq, Hkv, L, (L, Hq * 64), (1, Hq, L)
-    B, Hq, L, _ = q.shape
-    Hkv = k.shape[1]
-    _want("k", k, q.dtype, (B, Hkv, L, 64))
-    _want("v", v, q.dtype, (B, Hkv, L, 64))
+        return cu_seqlens.numel() - 1, Hq, Hkv, L, (L, Hq * 64), (1, Hq, L)
+    B, Hq, L, _ = shape
+    Hkv = kv[1]
+    if kv != (B, Hkv, L, 64):
+        raise ValueError("k: expected (%d, Hkv, %d, 64), got %s" % (B, L, tuple(kv)))
     if seq_lens is not None:
         _want("seq_lens", seq_lens, torch.int32, (B,))
-    return False, B, Hq, Hkv, L, (B, L, Hq * 64), (B, Hq, L)
+    return B, Hq, Hkv, L, (B, L, Hq * 64), (B, Hq, L)
 
 
 def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 0.125, cu_seqlens=None,
@@ -491,14 +513,13 @@ def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 
     cu_seqlens [n + 1] int32.  Returns (out [B, L, Hq*64] or [T, Hq*64], lse
     [B, Hq, L] or [1, Hq, T] float32, for the backward pass)."""
     _int32(w=w, sinks=sinks)
-    packed, n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
+    n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
     with _on(q, stream, k, v, cu_seqlens, seq_lens, out, lse):
-        out = torch.empty(o_shape, dtype=q.dtype, device=q.device) if out is None else _want("out", out, q.dtype, o_shape)
-        lse = (torch.empty(l_shape, dtype=torch.float32, device=q.device) if lse is None
-               else _want("lse", lse, torch.float32, l_shape))
+        out = _new(out, q, q.dtype, o_shape, "out")
+        lse = _new(lse, q, torch.float32, l_shape, "lse")
         st = lib().lf_window_attention_forward(
-            _heads("q", q), _heads("k", k), _heads("v", v), _dense(cu_seqlens), _dense(seq_lens), n, Hq, Hkv, L, w, sinks,
-            scale, DTYPE_CODE.get(q.dtype, 99), _raw_stream(stream, q), _dense(out), _dense(lse))
+            _heads("q", q), _heads("k", k), _heads("v", v), _dense(cu_seqlens), _dense(seq_lens), n, Hq, Hkv, L, w,
+            sinks, scale, DTYPE_CODE.get(q.dtype, 99), _raw_stream(stream, q), _dense(out), _dense(lse))
     _check(st, "lf_window_attention_forward")
     return out, lse
 
@@ -516,41 +537,43 @@ def lf_window_attention_backward(q, k, v, out, lse, dout, w: int, sinks: int = 0
     views (of one gradient of a fused projection, say); without them they are
     allocated like q, k, v, contiguous.  Returns (dq, dk, dv)."""
     _int32(w=w, sinks=sinks)
-    packed, n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
-    _want("out", out, q.dtype, o_shape)
-    _want("dout", dout, q.dtype, o_shape)
+    n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
+    dtype = q.dtype
+    _want("out", out, dtype, o_shape)
+    _want("dout", dout, dtype, o_shape)
     _want("lse", lse, torch.float32, l_shape)
     with _on(q, stream, k, v, out, lse, dout, cu_seqlens, seq_lens, dq, dk, dv, workspace):
-        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) if g is None else g
-                      for g, t in ((dq, q), (dk, k), (dv, v)))
-        need = lf_window_attention_backward_workspace_bytes(packed, n, Hq, Hkv, L, w, sinks)
+        dq, dk, dv = (t.new_empty(t.shape) if g is None else g for g, t in ((dq, q), (dk, k), (dv, v)))
+        need = 0
         if workspace is None:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            need = max(256, lib().lf_window_attention_backward_workspace_bytes(
+                int(cu_seqlens is not None), n, Hq, Hkv, L, w, sinks))
+        workspace, ws, ws_bytes = _workspace(workspace, q, need)
         st = lib().lf_window_attention_backward(
-            _heads("q", q), _heads("k", k), _heads("v", v), _dense(out), _dense(lse), _dense(dout), _dense(cu_seqlens),
-            _dense(seq_lens), n, Hq, Hkv, L, w, sinks, scale, DTYPE_CODE.get(q.dtype, 99), _dense(workspace),
-            workspace.numel() * workspace.element_size(), _raw_stream(stream, q), _heads("dq", dq, q.dtype, q.shape),
-            _heads("dk", dk, q.dtype, k.shape), _heads("dv", dv, q.dtype, v.shape))
+            _heads("q", q), _heads("k", k), _heads("v", v), _dense(out), _dense(lse), _dense(dout),
+            _dense(cu_seqlens), _dense(seq_lens), n, Hq, Hkv, L, w, sinks, scale, DTYPE_CODE.get(dtype, 99), ws,
+            ws_bytes, _raw_stream(stream, q), _heads("dq", dq, q.shape, dtype), _heads("dk", dk, k.shape, dtype),
+            _heads("dv", dv, k.shape, dtype))
     _check(st, "lf_window_attention_backward")
     return dq, dk, dv
 
 
 def _paged_shape(new, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
     """(n_seqs, T, Hkv, max_pages, num_pages, page_size)"""
-    if new.dim() != 3:
+    cache, dtype, i32 = k_cache.shape, new.dtype, torch.int32
+    if new.dim() != 3 or new.shape[2] != 64:
         raise ValueError("expected packed [T, H, 64], got %s" % (tuple(new.shape),))
-    if k_cache.dim() != 4 or k_cache.shape[-1] != 64:
-        raise ValueError("k_cache: expected [num_pages, Hkv, page_size, 64], got %s" % (tuple(k_cache.shape),))
-    _want("k_cache", k_cache, new.dtype)
-    _want("v_cache", v_cache, new.dtype, k_cache.shape)
-    if block_table.dim() != 2:
-        raise ValueError("block_table: expected [n_seqs, max_pages]")
+    if len(cache) != 4 or cache[3] != 64 or v_cache.shape != cache:
+        raise ValueError("k_cache, v_cache: expected two [num_pages, Hkv, page_size, 64], got %s and %s"
+                         % (tuple(cache), tuple(v_cache.shape)))
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise ValueError("k_cache, v_cache: expected %s, got %s and %s" % (dtype, k_cache.dtype, v_cache.dtype))
+    if block_table.dim() != 2 or block_table.dtype is not i32:
+        raise ValueError("block_table: expected [n_seqs, max_pages] int32")
     n, max_pages = block_table.shape
-    _want("block_table", block_table, torch.int32)
-    _want("cu_seqlens", cu_seqlens, torch.int32, (n + 1,))
-    _want("kv_lens", kv_lens, torch.int32, (n,))
-    num_pages, Hkv, page_size, _ = k_cache.shape
-    return n, new.shape[0], Hkv, max_pages, num_pages, page_size
+    _want("cu_seqlens", cu_seqlens, i32, (n + 1,))
+    _want("kv_lens", kv_lens, i32, (n,))
+    return n, new.shape[0], cache[1], max_pages, cache[0], cache[2]
 
 
 def lf_paged_cache_append(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, stream=None):
@@ -559,7 +582,7 @@ def lf_paged_cache_append(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_le
     the paged cache k_cache, v_cache [num_pages, Hkv, page_size, 64] (any
     strides) through block_table [n, max_pages] int32."""
     n, T, Hkv, max_pages, num_pages, page_size = _paged_shape(k, k_cache, v_cache, block_table, cu_seqlens, kv_lens)
-    _want("k", k, None, (T, Hkv, 64))
+    _want("k", k, k.dtype, (T, Hkv, 64))
     _want("v", v, k.dtype, (T, Hkv, 64))
     with _on(k, stream, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
         st = lib().lf_paged_cache_append(
@@ -585,32 +608,32 @@ def lf_paged_attention_forward(q, k_cache, v_cache, block_table, cu_seqlens, kv_
     _int32(w=w, sinks=sinks, max_q_len=max_q_len)
     Hq = q.shape[1]
     with _on(q, stream, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, workspace):
-        out = (torch.empty(T, Hq * 64, dtype=q.dtype, device=q.device) if out is None
-               else _want("out", out, q.dtype, (T, Hq * 64)))
-        need = lf_paged_attention_workspace_bytes(n, Hq, Hkv, T, max_q_len, max_pages, page_size, w, sinks)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        out = _new(out, q, q.dtype, (T, Hq * 64), "out")
+        need = 0
+        if workspace is None:
+            need = lib().lf_paged_attention_workspace_bytes(n, Hq, Hkv, T, max_q_len, max_pages, page_size, w, sinks)
+        workspace, ws, ws_bytes = _workspace(workspace, q, need)
         st = lib().lf_paged_attention_forward(
             _heads("q", q), _heads("k_cache", k_cache), _heads("v_cache", v_cache), _dense(block_table),
             _dense(cu_seqlens), _dense(kv_lens), n, Hq, Hkv, T, max_q_len, max_pages, num_pages, page_size, w, sinks,
-            scale, DTYPE_CODE.get(q.dtype, 99), _dense(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(stream, q), _dense(out))
+            scale, DTYPE_CODE.get(q.dtype, 99), ws, ws_bytes, _raw_stream(stream, q), _dense(out))
     _check(st, "lf_paged_attention_forward")
     return out
 
 
 def _rows(name, t):
-    """(pointer, rows, N, row stride) of [..., N]: contiguous, or 2-D with a
+    """(address, rows, N, row stride) of [..., N]: contiguous, or 2-D with a
     contiguous last dimension."""
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError("%s: expected [..., N]" % name)
-    N = t.shape[-1]
+    N = shape[-1]
     rows = t.numel() // N if N else 0
-    if t.dim() == 2 and (t.stride(1) == 1 or N == 1) and not t.is_contiguous():
+    if t.is_contiguous():
+        return t.data_ptr(), rows, N, N
+    if len(shape) == 2 and (t.stride(1) == 1 or N == 1):
         return t.data_ptr(), rows, N, t.stride(0)
-    if not t.is_contiguous():
-        raise ValueError("%s: expected a contiguous tensor, or a 2-D one with a row stride" % name)
-    return t.data_ptr(), rows, N, N
+    raise ValueError("%s: expected a contiguous tensor, or a 2-D one with a row stride" % name)
 
 
 def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
@@ -619,15 +642,19 @@ def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None,
     pass."""
     with _on(x, stream, gamma, beta, out, mean, rstd):
         px, rows, N, stride = _rows("x", x)
-        for name, t in (("gamma", gamma), ("beta", beta)):
-            if t is not None:
-                _want(name, t, torch.float32, (N,))
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else _want("out", out, x.dtype, x.shape)
-        mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) if t is None
-                      else _want(name, t, torch.float32, (rows,)) for name, t in (("mean", mean), ("rstd", rstd)))
+        if gamma is not None:
+            _want("gamma", gamma, torch.float32, (N,))
+        if beta is not None:
+            _want("beta", beta, torch.float32, (N,))
+        out = _new(out, x, x.dtype, x.shape, "out")
+        if mean is None and rstd is None:
+            mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind(0)
+        else:
+            mean = _new(mean, x, torch.float32, (rows,), "mean")
+            rstd = _new(rstd, x, torch.float32, (rows,), "rstd")
         st = lib().lf_layer_norm_forward(px, stride, _dense(gamma), _dense(beta), rows, N, eps,
-                                         DTYPE_CODE.get(x.dtype, 99), _raw_stream(stream, x), _dense(out), _dense(mean),
-                                         _dense(rstd))
+                                         DTYPE_CODE.get(x.dtype, 99), _raw_stream(stream, x), _dense(out),
+                                         _dense(mean), _dense(rstd))
     _check(st, "lf_layer_norm_forward")
     return out, mean, rstd
 
@@ -648,19 +675,17 @@ def lf_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta
             _want("gamma", gamma, torch.float32, (N,))
         _want("mean", mean, torch.float32, (rows,))
         _want("rstd", rstd, torch.float32, (rows,))
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else _want("dx", dx, x.dtype, x.shape)
-        if param_grads:
-            dgamma, dbeta = (torch.empty(N, dtype=torch.float32, device=x.device) if t is None else t
-                             for t in (dgamma, dbeta))
-        for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
-            if t is not None:
-                _want(name, t, torch.float32, (N,))
+        dx = _new(dx, x, x.dtype, x.shape, "dx")
+        if param_grads or dgamma is not None:
+            dgamma = _new(dgamma, x, torch.float32, (N,), "dgamma")
+        if param_grads or dbeta is not None:
+            dbeta = _new(dbeta, x, torch.float32, (N,), "dbeta")
+        need = 0
         if workspace is None and (dgamma is not None or dbeta is not None):
-            workspace = torch.empty(max(256, lf_layer_norm_backward_workspace_bytes(rows, N)), dtype=torch.uint8,
-                                    device=x.device)
+            need = max(256, lib().lf_layer_norm_backward_workspace_bytes(rows, N))
+        workspace, ws, ws_bytes = _workspace(workspace, x, need)
         st = lib().lf_layer_norm_backward(
-            pdy, dys, px, xs, _dense(gamma), _dense(mean), _dense(rstd), rows, N, DTYPE_CODE.get(x.dtype, 99),
-            _dense(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _raw_stream(stream, x), _dense(dx), _dense(dgamma), _dense(dbeta))
+            pdy, dys, px, xs, _dense(gamma), _dense(mean), _dense(rstd), rows, N, DTYPE_CODE.get(x.dtype, 99), ws,
+            ws_bytes, _raw_stream(stream, x), _dense(dx), _dense(dgamma), _dense(dbeta))
     _check(st, "lf_layer_norm_backward")
     return dx, dgamma, dbeta
