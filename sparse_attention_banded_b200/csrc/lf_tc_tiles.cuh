@@ -145,16 +145,20 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Half a row: 32 16-bit values from 32 floats.
 template <typename T>
-__device__ __forceinline__ void store_row32(T* p, const float* o, float scale) {
+__device__ __forceinline__ void store_row32(T* p, const float* o) {
     uint4* d = reinterpret_cast<uint4*>(p);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-        d[c] = make_uint4(Pair<T>::pack(o[8 * c] * scale, o[8 * c + 1] * scale),
-                          Pair<T>::pack(o[8 * c + 2] * scale, o[8 * c + 3] * scale),
-                          Pair<T>::pack(o[8 * c + 4] * scale, o[8 * c + 5] * scale),
-                          Pair<T>::pack(o[8 * c + 6] * scale, o[8 * c + 7] * scale));
+        d[c] = make_uint4(Pair<T>::pack(o[8 * c], o[8 * c + 1]), Pair<T>::pack(o[8 * c + 2], o[8 * c + 3]),
+                          Pair<T>::pack(o[8 * c + 4], o[8 * c + 5]), Pair<T>::pack(o[8 * c + 6], o[8 * c + 7]));
 }
 template <typename T>
 __device__ __forceinline__ void zero_row64(T* p) {

@@ -320,7 +320,9 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
             tmem_ld32f(tmQ + lane_off + half * 32, o);
             tmem_ld_wait();
             regs_ready<32>(o);
-            if (live) store_row32(dq, o, a.scale);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= a.scale;
+            if (live) store_row32(dq, o);
             else if (stored)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(dq)[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -565,15 +567,18 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
                 tmem_ld32f((w ? tmV : tmK) + lane_off + half * 32, o);
                 tmem_ld_wait();
                 regs_ready<32>(o);
-                const float f = w ? 1.0f : a.scale;
+                if (w == 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= a.scale;
+                }
                 if (to.part) {
                     float4* d = reinterpret_cast<float4*>(to.part + w * kD);
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
-                        d[u] = make_float4(o[4 * u] * f, o[4 * u + 1] * f, o[4 * u + 2] * f, o[4 * u + 3] * f);
+                        d[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
                 } else if (to.dk) {
                     T* d = w ? to.dv : to.dk;
-                    if (key < n_keys) store_row32(d, o, f);
+                    if (key < n_keys) store_row32(d, o);
                     else
 #pragma unroll
                         for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(d)[u] = make_uint4(0u, 0u, 0u, 0u);

@@ -520,10 +520,9 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 tc_fence_after();
                 const float2 u0 = ml[r], u1 = ml[kBM + r];
                 const float top = fmaxf(u0.x, u1.x), base = top == -INFINITY ? 0.0f : top;
-                const float f0 = ex2(u0.x - base), f1 = ex2(u1.x - base);
-                const float sum = i >= 0 ? u0.y * f0 + u1.y * f1 : 0.0f;  // i < 0: no token of the sequence
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
+                const float f0 = ex2(u0.x - base), f1 = ex2(u1.x - base), sum = u0.y * f0 + u1.y * f1;
+                const bool none = i < 0 || sum == 0.0f;  // no token of the sequence, or no key
+                const float inv = rcp_approx(sum), lse2 = none ? -INFINITY : top + lg2_approx(sum);
                 const size_t orow = ((size_t)p->batch * L + p->start + tok) * a.Hq + p->hk * G + r_head;
                 float o[32], o1[32];
                 tmem_ld32f(t_lane + kTmemO + half * 32, o);
@@ -532,19 +531,26 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 regs_ready<32>(o);
                 regs_ready<32>(o1);
                 tc_fence_before();
-                // (a half that saw no key holds exact zeros)
+                const float2 g0 = make_float2(f0 * inv, f0 * inv), g1 = make_float2(f1 * inv, f1 * inv);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = sum == 0.0f ? 0.0f : o[e] * f0 + o1[e] * f1;
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 v = ffma2(make_float2(o[e], o[e + 1]), g0, fmul2(make_float2(o1[e], o1[e + 1]), g1));
+                    o[e] = v.x;
+                    o[e + 1] = v.y;
+                }
+                if (none) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                }
                 if (row_stored) {
                     if (kPaged && p->part) {
                         const size_t at = (size_t)p->z * ((size_t)L * a.Hq) + orow;
                         float4* d = reinterpret_cast<float4*>(pp.o + at * kD + half * 32);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            d[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+                        for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         if (half == 0) pp.lse[at] = lse2;
                     } else {
-                        store_row32(static_cast<T*>(a.out) + orow * kD + half * 32, o, inv);
+                        store_row32(static_cast<T*>(a.out) + orow * kD + half * 32, o);
                         if constexpr (!kPaged) {
                             if (half == 0)
                                 a.lse[((size_t)p->batch * a.Hq + p->hk * G + r_head) * L + p->start + tok] = lse2 * kLn2;
