@@ -252,13 +252,47 @@ decode_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Paged
     }
 }
 
-// One warp per row of out: joins the chunks of rows that have several.
-template <typename T>
+// Partials of one row: the weighted sum of some of them.
+struct Joined {
+    float top, sum;
+    float2 x;  // elements 2 lane, 2 lane + 1
+};
+// `count` partials `step` rows apart, every `stride`-th from `from` on.
+__device__ __forceinline__ Joined join(const float* o, const float* e, size_t step, int count, int from, int stride) {
+    const int lane = threadIdx.x & 31;
+    Joined j = {-INFINITY, 0.f, make_float2(0.f, 0.f)};
+    for (int s = from + lane * stride; s < count; s += 32 * stride) j.top = fmaxf(j.top, e[s * step]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) j.top = fmaxf(j.top, __shfl_xor_sync(0xffffffffu, j.top, d));
+    const float base = j.top == -INFINITY ? 0.f : j.top;
+#pragma unroll 8
+    for (int s = from; s < count; s += stride) {
+        const float f = ex2(e[s * step] - base);
+        const float2 v = *reinterpret_cast<const float2*>(o + s * step * kD + 2 * lane);
+        j.sum += f;
+        j.x.x = fmaf(f, v.x, j.x.x);
+        j.x.y = fmaf(f, v.y, j.x.y);
+    }
+    return j;
+}
+__device__ __forceinline__ Joined join2(const Joined& a, const Joined& b) {
+    Joined j;
+    j.top = fmaxf(a.top, b.top);
+    const float base = j.top == -INFINITY ? 0.f : j.top, fa = ex2(a.top - base), fb = ex2(b.top - base);
+    j.sum = a.sum * fa + b.sum * fb;
+    j.x = make_float2(a.x.x * fa + b.x.x * fb, a.x.y * fa + b.x.y * fb);
+    return j;
+}
+
+// Joins the pieces of rows that have several, kPerRow of a block's 8 warps
+// per row of out: all of them where a context may be cut into many.
+template <typename T, int kPerRow>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedPlan pl) {
+    __shared__ Joined parts[8][32];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPerRow;
+    const long long row = (long long)blockIdx.x * (8 / kPerRow) + warp / kPerRow;
     if (row >= (long long)a.T * a.Hq) return;
     const int tok = (int)(row / a.Hq), G = a.Hq / a.Hkv;
     const int b = seq_of_token_warp(a.cu, a.n_seqs, tok);
@@ -266,32 +300,25 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     if (tok < start || tok >= start + n) return;
     int kv, first;
     if (!paged_seq(a, b, n, kv, first, false)) return;
-    int chunks;
+    int pieces;
     if (pl.decode && n * G <= kRows) {
-        chunks = (decode_tiles(first, n, kv, a.w, a.sinks).n + pl.chunk - 1) / pl.chunk;
+        pieces = (decode_tiles(first, n, kv, a.w, a.sinks).n + pl.chunk - 1) / pl.chunk;
     } else {
         const int TQ = 128 / G, t0 = (tok - start) / TQ * TQ;
-        chunks = (tile_key_blocks(first, t0, imin(t0 + TQ, n), kv, a.w, a.sinks).n + pl.per - 1) / pl.per;
+        pieces = (tile_key_blocks(first, t0, imin(t0 + TQ, n), kv, a.w, a.sinks).n + pl.per - 1) / pl.per;
     }
-    if (chunks <= 1) return;
-    const size_t step = (size_t)a.T * a.Hq;
-    float top = -INFINITY;
-    for (int s = lane; s < chunks; s += 32) top = fmaxf(top, pl.lse[s * step + row]);
+    if (pieces <= 1) return;  // written whole
+    Joined j = join(pl.o + row * kD, pl.lse + row, (size_t)a.T * a.Hq, pieces, part, kPerRow);
+    if constexpr (kPerRow > 1) {
+        static_assert(kPerRow == 8, "one row per block");
+        parts[warp][lane] = j;
+        __syncthreads();
+        if (warp > 0) return;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    float2 x = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < chunks; ++s) {
-        const float f = ex2(pl.lse[s * step + row] - base);
-        const float2 v = *reinterpret_cast<const float2*>(pl.o + (s * step + row) * kD + 2 * lane);
-        sum += f;
-        x.x = fmaf(f, v.x, x.x);
-        x.y = fmaf(f, v.y, x.y);
+        for (int u = 1; u < 8; ++u) j = join2(j, parts[u][lane]);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * kD)[lane] = Pair<T>::pack(x.x * inv, x.y * inv);
+    const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
+    reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * kD)[lane] = Pair<T>::pack(j.x.x * inv, j.x.y * inv);
 }
 
 template <typename T>
@@ -301,9 +328,14 @@ lf_status paged_t(const PagedArgs& a, const PagedPlan& pl, cudaStream_t stream) 
         st = launch_pdl(decode_kernel<T>, dim3((unsigned)a.n_seqs * pl.decode_splits, a.Hkv), dim3(kWarps * 32),
                         (size_t)pl.chunk * sizeof(int2), stream, a, pl);
     if (st == LF_OK && pl.tensor) st = launch_paged_tc(a, pl, stream);
-    if (st == LF_OK && pl.splits() > 1)
-        st = launch_pdl(merge_kernel<T>, dim3((unsigned)(((long long)a.T * a.Hq + 7) / 8)), dim3(256), 0, stream, a, pl);
-    return st;
+    if (st != LF_OK || pl.splits() <= 1) return st;
+    // A block per row for more than 16 pieces and no more blocks than run at
+    // once (98 pieces of one context of 100000: 80 us by a warp per row, 23
+    // by a block).
+    const long long rows = (long long)a.T * a.Hq;
+    if (pl.splits() > 16 && rows <= 8 * 148)
+        return launch_pdl(merge_kernel<T, 8>, dim3((unsigned)rows), dim3(256), 0, stream, a, pl);
+    return launch_pdl(merge_kernel<T, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, a, pl);
 }
 
 }  // namespace

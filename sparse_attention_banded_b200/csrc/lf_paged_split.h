@@ -63,10 +63,11 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
     if (p.tensor) {
         // Rounds of the 2 x 148 resident CTAs times blocks per item; pieces
         // are joined by a further kernel, worth about 12 blocks (3 when it
-        // runs anyway).
-        const long long blocks = most_blocks(max_q, width, w, sinks, 64);
+        // runs anyway, for the decode kernel).  Next to single tokens, which
+        // are no tiles, a quarter of the sequences are taken to end in one.
         const int join = p.decode && p.decode_splits > 1 ? 3 : 12;
-        const long long tiles = (long long)packed_slots(T, n_seqs, 128 / G) * Hkv;
+        const long long blocks = most_blocks(max_q, width, w, sinks, 64);
+        const long long tiles = ((long long)T / (128 / G) + (p.decode ? (n_seqs + 3) / 4 : n_seqs)) * Hkv;
         long long best = -1;
         for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
             const long long per = (blocks + s - 1) / s, rounds = (tiles * s + 295) / 296;
