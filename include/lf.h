@@ -426,6 +426,10 @@ lf_status lf_selftest_bounded_wait(unsigned long long limit_ns, lf_stream_t stre
  * and rows of an output view must not overlap.  The stride of a dimension
  * of size 1 is not used.  So [B, H, L, 64], [T, H, 64] and slices of a fused
  * projection's output all fit.
+ *
+ * The calls from here on keep no state of their own between calls.  The
+ * first call of the library on a device allocates its status word: make it
+ * before any stream capture; every call after that may be captured.
  */
 typedef struct {
     void* data;
@@ -547,7 +551,8 @@ size_t lf_paged_attention_workspace_bytes(int n_seqs, int Hq, int Hkv, int T, in
  * clamped and recorded as LF_ERR_BAD_LENGTHS.
  * Errors: LF_ERR_NULL, LF_ERR_BAD_DIM, LF_ERR_DTYPE, LF_ERR_MISALIGNED,
  * LF_ERR_TOO_LARGE (T * Hq >= 2^31, max_pages * page_size > 2^24, n_seqs >=
- * 2^21, Hkv > 65535), LF_ERR_WORKSPACE.  T = 0 does nothing.  Asynchronous.
+ * 2^21, Hkv > 65535, or more pieces of work than a grid holds),
+ * LF_ERR_WORKSPACE.  T = 0 does nothing.  Asynchronous.
  */
 lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache, const lf_heads* v_cache,
                                      const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* kv_lens,

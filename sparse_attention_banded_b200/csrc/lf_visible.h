@@ -123,16 +123,10 @@ LF_HD bool range_visible(int i0, int i1, int j0, int j1, int w, int sinks) {
     return i0 - j1 <= w || j0 < sinks;
 }
 
-// Bits [0, n) / [lo, hi) of a 64-bit word, arguments clamped to [0, 64].
+// Bits [0, n) of a 64-bit word, n clamped to [0, 64].
 LF_HD unsigned long long low_bits64(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
-// Keys c0 .. c0 + 63 that the query at position i sees, of n_keys.
-LF_HD unsigned long long visible_bits(int i, int c0, int n_keys, int w, int sinks) {
-    const unsigned long long causal = low_bits64(imin(i + 1, n_keys) - c0);
-    return causal & (~low_bits64(i - w - c0) | low_bits64(sinks - c0));
-}
-
 // Bits [0, n) of a 32-bit word, n clamped to [0, 32].
 LF_HD unsigned low_bits32(int n) {
 #ifdef __CUDA_ARCH__
@@ -143,7 +137,7 @@ LF_HD unsigned low_bits32(int n) {
     return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
 #endif
 }
-// The same as visible_bits for the 32 keys from c0 on.
+// Keys c0 .. c0 + 31 that the query at position i sees, of n_keys.
 LF_HD unsigned visible_bits32(int i, int c0, int n_keys, int w, int sinks) {
     return low_bits32(imin(i + 1, n_keys) - c0) & (~low_bits32(i - w - c0) | low_bits32(sinks - c0));
 }

@@ -261,6 +261,7 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
     a.out = out;
     a.status = d->status;
     PagedPlan plan = paged_plan(n_seqs, Hq, Hkv, T, a.max_q, max_pages * page_size, a.w, a.sinks);
+    if (plan.decode && (long long)n_seqs * plan.decode_splits >= kInt31) return LF_ERR_TOO_LARGE;
     plan.o = static_cast<float*>(workspace);
     plan.lse = plan.o + align256((size_t)plan.splits() * T * Hq * 64 * sizeof(float)) / sizeof(float);
     return launch_paged_forward(a, plan, (cudaStream_t)stream);

@@ -379,3 +379,57 @@ def test_training_block_gradients():
     for n, t in got.items():
         want = yy.detach() if n == "y" else L[n].grad
         assert float((t.double() - want).abs().max()) <= 8 * 512 * 2.0 ** -24 * float(want.abs().max()), n
+
+
+def test_sequences_share_pages():
+    """Two sequences forked from one prompt: the same pages in both tables,
+    each with a last page of its own."""
+    c = Case([1, 5], [133, 140], 4, 2, 16, seed=20)
+    c.k[1][:, :128], c.v[1][:, :128] = c.k[0][:, :128], c.v[0][:, :128]
+    c.table[1, :8] = c.table[0, :8]
+    c.run().check()
+
+
+def test_two_calls_at_once():
+    """Two batches on two streams, workspaces of their own."""
+    cases = [Case([1, 30, 1], [900, 500, 3000], 8, 2, 16, seed=21 + i, w=700, sinks=2) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, st in zip(cases, streams):
+            lf.lf_paged_cache_append(c.kn, c.vn, c.kc, c.vc, c.table, c.cu, c.kv, stream=st)
+            lf.lf_paged_attention_forward(c.q, c.kc, c.vc, c.table, c.cu, c.kv, 30, c.w, c.sinks, out=c.out, stream=st)
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
+
+
+def test_cache_of_more_than_2_31_elements():
+    """Pages whose offsets pass 32 bits (a pool of 2.6e9 elements a cache;
+    only the pages in use are written)."""
+    pages, Hkv, page = 80000, 8, 64
+    kc, vc = (torch.empty(pages, Hkv, page, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(22)
+    qlens, kvlens = [1, 40], [200, 100]
+    table = torch.tensor([[79999, 3, 70001, 66000], [65537, 79998, 5, 6]], dtype=torch.int32).cuda()
+    k, v = ([torch.randn(Hkv, m, 64, generator=g).half().cuda() for m in kvlens] for _ in range(2))
+    kv = torch.tensor(kvlens, dtype=torch.int32).cuda()
+    for b, m in enumerate(kvlens):
+        lf.lf_paged_cache_append(k[b].transpose(0, 1), v[b].transpose(0, 1), kc, vc, table[b:b + 1].contiguous(),
+                                 torch.tensor([0, m], dtype=torch.int32).cuda(), kv[b:b + 1].clone())
+    q = torch.randn(41, 16, 64, generator=g).half().cuda()
+    cu = torch.tensor([0, 1, 41], dtype=torch.int32).cuda()
+    out = lf.lf_paged_attention_forward(q, kc, vc, table, cu, kv, 40)
+    at = 0
+    for b, (n, m) in enumerate(zip(qlens, kvlens)):
+        r = reference(q[at:at + n].transpose(0, 1), k[b], v[b], m - n, 1 << 29, 0)
+        check("sequence %d" % b, out[at:at + n].view(n, 16, 64).transpose(0, 1), r["out"], r["b_out"])
+        at += n
+
+
+def test_one_context_in_many_pieces():
+    """A context cut into more pieces than one warp joins (a block per row),
+    and a table whose pieces are mostly empty."""
+    Case([1], [40000], 2, 1, 64, seed=23).run().check()
+    Case([1, 1], [40000, 30], 4, 1, 64, seed=24, w=30000, sinks=3).run().check()
+    Case([1], [100], 4, 1, 64, seed=25, extra=1000).run().check()

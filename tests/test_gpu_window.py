@@ -298,3 +298,38 @@ def test_no_tokens():
     assert out.shape == (0, 128) and lse.shape == (1, 2, 0)
     g = lf.lf_window_attention_backward(z, z, z, out, lse, out, 4, cu_seqlens=cu)
     assert all(t.shape == (0, 2, 64) for t in g)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_rows_more_than_2_31_elements_apart(dtype):
+    """Keys and values (and their gradients) in rows 2^25 elements apart: the
+    last of 100 starts past 2^31."""
+    T, step = 100, 1 << 25
+    big = [torch.empty(T * step, dtype=DT[dtype], device="cuda").as_strided((T, 1, 64), (step, 64, 1)) for _ in range(2)]
+    q, k, v = (_rand((T, 1, 64), dtype, 110 + i) for i in range(3))
+    do = _rand((T, 64), dtype, 113)
+    cu = torch.tensor([0, T], dtype=torch.int32).cuda()
+    want_o, lse = lf.lf_window_attention_forward(q, k, v, 30, 2, cu_seqlens=cu)
+    want = lf.lf_window_attention_backward(q, k, v, want_o, lse, do, 30, 2, cu_seqlens=cu)
+    big[0].copy_(k)
+    out, lse = lf.lf_window_attention_forward(q, big[0], v, 30, 2, cu_seqlens=cu)
+    got = lf.lf_window_attention_backward(q, big[0], v, out, lse, do, 30, 2, cu_seqlens=cu, dk=big[1])
+    assert torch.equal(out, want_o)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_heads_share_storage_with_the_output_of_a_projection():
+    """q, k and v as interleaved slices of one [B, L, H, 3, 64] buffer, and
+    gradients into slices of another."""
+    B, L, H = 2, 150, 3
+    x = _rand((B, L, H, 3, 64), "bf16", 120)
+    q, k, v = (x[:, :, :, i].transpose(1, 2) for i in range(3))
+    out, lse = lf.lf_window_attention_forward(q, k, v, 40, 4)
+    do = _rand((B, L, H * 64), "bf16", 121)
+    dx = torch.full_like(x, 7.0)
+    g = [dx[:, :, :, i].transpose(1, 2) for i in range(3)]
+    lf.lf_window_attention_backward(q, k, v, out, lse, do, 40, 4, dq=g[0], dk=g[1], dv=g[2])
+    rows = lambda t: t.view(B, L, H, 64).transpose(1, 2)  # noqa: E731
+    _compare([dict(out=rows(out)[b], lse=lse[b], dq=g[0][b], dk=g[1][b], dv=g[2][b]) for b in range(B)],
+             [(q[b], k[b], v[b], rows(do)[b]) for b in range(B)], 40, 4)

@@ -28,7 +28,7 @@ void blocks(int i0, int i1, int nk, int w, int s, int bk, int* o) {
 }
 int full(int i0, int i1, int j0, int bk, int nk, int w, int s) { return block_full(i0, i1, j0, bk, nk, w, s); }
 int range_vis(int i0, int i1, int j0, int j1, int w, int s) { return range_visible(i0, i1, j0, j1, w, s); }
-unsigned long long bits(int i, int c0, int nk, int w, int s) { return visible_bits(i, c0, nk, w, s); }
+unsigned long long low64(int n) { return low_bits64(n); }
 unsigned bits32(int i, int c0, int nk, int w, int s) { return visible_bits32(i, c0, nk, w, s); }
 void plan(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int* o) {
     PagedPlan p = paged_plan(n, Hq, Hkv, T, mq, width, w, s);
@@ -49,7 +49,7 @@ def P(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-fsanitize=undefined",
                     "-fno-sanitize-recover=undefined", "-I", build.CSRC, str(d / "plan.cpp"), "-o", so], check=True)
     L = ctypes.CDLL(so)
-    L.bits.restype, L.bits32.restype = ctypes.c_ulonglong, ctypes.c_uint
+    L.low64.restype, L.bits32.restype = ctypes.c_ulonglong, ctypes.c_uint
     return L
 
 
@@ -134,9 +134,12 @@ def test_key_blocks_and_masks(P, seed):
     for i in {i0, i1}:
         for c0 in range(0, nk, 64):
             want = sum(1 << t for t in range(64) if c0 + t < nk and _sees(i, c0 + t, w, s))
-            assert P.bits(i, c0, nk, w, s) == want
             assert P.bits32(i, c0, nk, w, s) == want & 0xffffffff and P.bits32(i, c0 + 32, nk, w, s) == want >> 32
             assert P.bits32(-1, c0, nk, w, s) == 0
+
+
+def test_low_bits(P):
+    assert [P.low64(n) for n in (-5, 0, 1, 63, 64, 70)] == [0, 0, 1, 2 ** 63 - 1, 2 ** 64 - 1, 2 ** 64 - 1]
 
 
 def test_pages_outside_the_table_are_missing(P):
