@@ -284,17 +284,19 @@ __device__ __forceinline__ Joined join2(const Joined& a, const Joined& b) {
     return j;
 }
 
-// Joins the pieces of rows that have several, kPerRow of a block's 8 warps
-// per row of out: all of them where a context may be cut into many.
-template <typename T, int kPerRow>
+// Joins the pieces of rows that have several.  kPerRow of a block's 8 warps
+// share a row (all of them where a context may be cut into many pieces), or
+// one warp takes kRowsEach rows (heads) of a token, looking its sequence up once.
+template <typename T, int kPerRow, int kRowsEach>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedPlan pl) {
     __shared__ Joined parts[8][32];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPerRow;
-    const long long row = (long long)blockIdx.x * (8 / kPerRow) + warp / kPerRow;
-    if (row >= (long long)a.T * a.Hq) return;
-    const int tok = (int)(row / a.Hq), G = a.Hq / a.Hkv;
+    const int each = (a.Hq + kRowsEach - 1) / kRowsEach;  // warps (or blocks) per token
+    const long long at = (long long)blockIdx.x * (8 / kPerRow) + warp / kPerRow;
+    if (at >= (long long)a.T * each) return;
+    const int tok = (int)(at / each), h0 = (int)(at % each) * kRowsEach, G = a.Hq / a.Hkv;
     const int b = seq_of_token_warp(a.cu, a.n_seqs, tok);
     const int start = iclamp(a.cu[b], 0, a.T), n = iclamp(a.cu[b + 1], 0, a.T) - start;
     if (tok < start || tok >= start + n) return;
@@ -308,17 +310,21 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         pieces = (tile_key_blocks(first, t0, imin(t0 + TQ, n), kv, a.w, a.sinks).n + pl.per - 1) / pl.per;
     }
     if (pieces <= 1) return;  // written whole
-    Joined j = join(pl.o + row * kD, pl.lse + row, (size_t)a.T * a.Hq, pieces, part, kPerRow);
-    if constexpr (kPerRow > 1) {
-        static_assert(kPerRow == 8, "one row per block");
-        parts[warp][lane] = j;
-        __syncthreads();
-        if (warp > 0) return;
+#pragma unroll 4
+    for (int h = h0; h < imin(h0 + kRowsEach, a.Hq); ++h) {
+        const size_t row = (size_t)tok * a.Hq + h;
+        Joined j = join(pl.o + row * kD, pl.lse + row, (size_t)a.T * a.Hq, pieces, part, kPerRow);
+        if constexpr (kPerRow > 1) {
+            static_assert(kPerRow == 8 && kRowsEach == 1, "one row per block");
+            parts[warp][lane] = j;
+            __syncthreads();
+            if (warp > 0) return;
 #pragma unroll
-        for (int u = 1; u < 8; ++u) j = join2(j, parts[u][lane]);
+            for (int u = 1; u < 8; ++u) j = join2(j, parts[u][lane]);
+        }
+        const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
+        reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * kD)[lane] = Pair<T>::pack(j.x.x * inv, j.x.y * inv);
     }
-    const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
-    reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * kD)[lane] = Pair<T>::pack(j.x.x * inv, j.x.y * inv);
 }
 
 template <typename T>
@@ -331,11 +337,15 @@ lf_status paged_t(const PagedArgs& a, const PagedPlan& pl, cudaStream_t stream) 
     if (st != LF_OK || pl.splits() <= 1) return st;
     // A block per row for more than 16 pieces and no more blocks than run at
     // once (98 pieces of one context of 100000: 80 us by a warp per row, 23
-    // by a block).
+    // by a block); eight rows a warp where there are more rows than warps
+    // (24 us by a warp each for 32768 rows).
     const long long rows = (long long)a.T * a.Hq;
     if (pl.splits() > 16 && rows <= 8 * 148)
-        return launch_pdl(merge_kernel<T, 8>, dim3((unsigned)rows), dim3(256), 0, stream, a, pl);
-    return launch_pdl(merge_kernel<T, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, a, pl);
+        return launch_pdl(merge_kernel<T, 8, 1>, dim3((unsigned)rows), dim3(256), 0, stream, a, pl);
+    if (rows <= 64 * 148)
+        return launch_pdl(merge_kernel<T, 1, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, a, pl);
+    const long long warps = (long long)a.T * ((a.Hq + 7) / 8);
+    return launch_pdl(merge_kernel<T, 1, 8>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, a, pl);
 }
 
 }  // namespace

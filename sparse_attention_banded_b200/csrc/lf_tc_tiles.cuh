@@ -83,21 +83,22 @@ __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 // D0 (+)= A[:, :32] B[:32], D1 (+)= A[:, 32:] B[32:]: A (128 x 64, 16-bit) in
-// tensor memory, its halves of 32 in 16 columns each, 32 columns apart; B 64
-// x 64, MN-major in shared memory.  D1 == D0 with accumulate_second: one sum.
+// tensor memory, its halves of 32 in 16 columns each, kApart columns apart;
+// B 64 x 64, MN-major in shared memory.  D1 == D0 with accumulate_second: one sum.
+template <int kApart = 32>
 __device__ __forceinline__ void mma4_ts(uint32_t d0, uint32_t d1, uint32_t a, uint64_t b, uint32_t idesc,
                                         uint32_t accumulate, uint32_t accumulate_second) {
     asm volatile(
         "{\n\t.reg .pred e, p, q, r;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 r, %6, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
-        "add.s32 a1, %2, 8;\n\tadd.s32 a2, %2, 32;\n\tadd.s32 a3, %2, 40;\n\t"
+        "add.s32 a1, %2, 8;\n\tadd.s32 a2, %2, %7;\n\tadd.s32 a3, %2, %8;\n\t"
         "add.s64 b1, %3, 128;\n\tadd.s64 b2, %3, 256;\n\tadd.s64 b3, %3, 384;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %3, %4, p;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [a2], b2, %4, r;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [a3], b3, %4, q;\n\t}" ::"r"(d0),
-        "r"(d1), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(accumulate_second)
+        "r"(d1), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(accumulate_second), "n"(kApart), "n"(kApart + 8)
         : "memory");
 }
 __device__ __forceinline__ void commit_elect(uint64_t* bar) {

@@ -8,21 +8,21 @@
 //     S = Q K^T                        (tcgen05.mma, fp32 in tensor memory)
 //     m' = max(m, max s), P = 2^(s - m'), l += sum P
 //     O = O 2^(m - m') + P V           (P from tensor memory)
-// Two threads share a row, each with its own half of every block's keys, its
-// own m, l and O: they meet only at the tile's end, as two pieces of a split
-// context would.  S has two buffers, so the next block's S runs under this
-// one's softmax; P overwrites the first 16 columns of its half of S.  S, S
-// and two O's take 256 tensor-memory columns: two CTAs per SM.  A block
-// takes a CTA about 2000 cycles, 800 of them arithmetic and the rest the
-// latencies of tensor-memory accesses and hand-offs, which the other CTA's
-// warps fill; a tile of its own launch paid 8000 cycles more to start and
-// end, so the loads, the plan and the first S of the next tile run under the
-// end of this one.
+// One thread per row; P overwrites the first half of S's columns.  S and O
+// take 128 tensor-memory columns: four CTAs per SM.  A CTA's block is a chain
+// of latencies (product, softmax, product, 2500 cycles of which the
+// arithmetic is a third), and the four chains fill each other's gaps.  (Two
+// threads a row with the next S under this softmax, two CTAs per SM: 70 us
+// instead of 59 for 4 x 4096 tokens, 16 heads, window 256.)  A tile of its
+// own launch paid 8000 cycles more to start and end, so CTAs are persistent
+// and the loads and plan of the next tile run under the end of this one.
+// The four softmax warps keep 64 scores a row in registers, of the share
+// that the other warps give up.
 // The O update is skipped unless a row's maximum grows by more than 2^8 (P
 // <= 2^8 then).  P is rounded to the storage type, the MMA's operand type;
 // sums stay fp32.
 //
-// Warps 0-7: softmax and epilogue, warp 8: TMA loads, warp 9: MMAs, warp 10:
+// Warps 0-3: softmax and epilogue, warp 4: TMA loads, warp 5: MMAs, warp 6:
 // the plans of the coming tiles (which sequence, which keys).  All waits are
 // bounded (LF_ERR_DEVICE_TIMEOUT).
 //
@@ -77,25 +77,24 @@ using namespace sm100;
 constexpr int kBM = 128;   // query rows
 constexpr int kBN = 64;    // keys per block
 constexpr int kD = 64;
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 constexpr int kRing = 4;   // plans ahead
-constexpr int kSoftmaxWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kPlanWarp = 10;
-constexpr int kThreads = 12 * 32;
-constexpr int kCtas = 2;   // per SM
-// 80 registers a thread at launch; a block's share is split anew.
-constexpr uint32_t kRegsLaunch = 80, kRegsProducer = 48, kRegsSoftmax = 96;
-static_assert(4 * 32 * kRegsProducer + 8 * 32 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr int kSoftmaxWarps = 4;
+constexpr int kTmaWarp = 4, kMmaWarp = 5, kPlanWarp = 6;
+constexpr int kThreads = 8 * 32;
+constexpr int kCtas = 4;   // per SM
+// 64 registers a thread at launch; a block's share is split anew.
+constexpr uint32_t kRegsLaunch = 64, kRegsProducer = 24, kRegsSoftmax = 104;
+static_assert(4 * 32 * kRegsProducer + 4 * 32 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kQBytes = kBM * kD * 2, kKBytes = kBN * kD * 2;
-constexpr uint32_t kOffK = 2 * kQBytes, kOffV = kOffK + kStages * kKBytes, kOffMl = kOffV + kStages * kKBytes;
-constexpr uint32_t kOffPlan = kOffMl + 2 * kBM * 8;              // after (m, l) of both halves
+constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffPlan = kOffV + kStages * kKBytes;
 constexpr uint32_t kPlanBytes = 80;
 constexpr uint32_t kOffBar = kOffPlan + kRing * kPlanBytes;
-constexpr uint32_t kBars = 4 + 2 * kStages + 7 + 2 * kRing;
+constexpr uint32_t kBars = 2 + 2 * kStages + 4 + 2 * kRing;
 constexpr uint32_t kOffMask = kOffBar + kBars * 8;               // valid keys of each stage (paged)
 constexpr uint32_t kOffMisc = kOffMask + kStages * 8;
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;            // + alignment slack
-constexpr uint32_t kTmemCols = 256, kTmemO = 128;                // S at 0 and 64, O at 128 and 192
+constexpr uint32_t kTmemCols = 128, kTmemO = 64;                 // S (then P) at 0, O at 64
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
 static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
@@ -178,18 +177,16 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
               int n_items) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // [2]
-    uint64_t* q_empty = q_full + 2;                                  // [2]
-    uint64_t* kv_full = q_empty + 2;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* kv_full = q_empty + 1;
     uint64_t* kv_empty = kv_full + kStages;
     uint64_t* s_full = kv_empty + kStages;
-    uint64_t* p_full = s_full + 2;  // (both [2]: per S buffer)
-    uint64_t* o_full = p_full + 2;
-    uint64_t* ml_full = o_full + 1;
-    uint64_t* drain = ml_full + 1;
+    uint64_t* p_full = s_full + 1;
+    uint64_t* o_full = p_full + 1;
+    uint64_t* drain = o_full + 1;
     uint64_t* plan_full = drain + 1;
     uint64_t* plan_empty = plan_full + kRing;
-    float2* ml = reinterpret_cast<float2*>(smem + kOffMl);
     volatile unsigned long long* valid = reinterpret_cast<volatile unsigned long long*>(smem + kOffMask);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
@@ -197,18 +194,15 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int u = 0; u < 2; ++u) {
-            mbar_init(&q_full[u], 1);
-            mbar_init(&q_empty[u], 1);
-            mbar_init(&s_full[u], 1);
-            mbar_init(&p_full[u], kSoftmaxWarps);
-        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(s_full, 1);
+        mbar_init(p_full, kSoftmaxWarps);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
         }
         mbar_init(o_full, 1);
-        mbar_init(ml_full, kSoftmaxWarps);
         mbar_init(drain, 1);
         for (int s = 0; s < kRing; ++s) {
             mbar_init(&plan_full[s], 1);
@@ -276,29 +270,51 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     break;
                 }
                 if (p->nb == 0) continue;
-                ok = warp_wait(&q_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag);
+                ok = warp_wait(q_empty, (it & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[it & 1], (uint32_t)(TQ * G) * kD * 2);
-                    tma_load_4d(smem + (it & 1) * kQBytes, &maps.q, &q_full[it & 1], 0, p->hk * G, p->start + p->t0, p->batch);
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(TQ * G) * kD * 2);
+                    tma_load_4d(smem, &maps.q, q_full, 0, p->hk * G, p->start + p->t0, p->batch);
                 }
                 ++it;
                 const int hk = p->hk, n_keys = p->n_keys, nb = p->nb;
+                // Paged: a lane looks up the page of one box, those of 32 /
+                // boxes blocks at a time and as many ahead.
+                [[maybe_unused]] int next_page = -1, next_pos = 0, page = -1, pos = 0, rows = 0, boxes = 1;
+                [[maybe_unused]] auto look_up = [&](int j) {
+                    if constexpr (kPaged) {
+                        j += lane / boxes;
+                        next_page = -1;
+                        if (j < nb) {
+                            next_pos = p->key0(j) + lane % boxes * rows;
+                            if (next_pos < n_keys) {
+                                next_page = page_of(a.table + (size_t)p->b * a.max_pages, a.max_pages, a.num_pages,
+                                                    a.page_shift, next_pos);
+                                if (next_page < 0 && range_visible(imax(p->i0, 0), p->i1, next_pos,
+                                                                   imin(next_pos + rows, n_keys) - 1, a.w, a.sinks))
+                                    record_status(a.status, p->b, LF_ERR_BAD_PAGE);
+                            }
+                        }
+                    }
+                };
+                if constexpr (kPaged) {
+                    rows = imin(kBN, 1 << a.page_shift);
+                    boxes = kBN / rows;
+                    look_up(0);
+                }
                 for (int j = 0; j < nb; ++j, ++g) {
                     const int s = g % kStages;
                     const int c0 = p->key0(j);
                     uint8_t *ks = smem + kOffK + s * kKBytes, *vs = smem + kOffV + s * kKBytes;
                     if constexpr (kPaged) {
-                        // lane u fetches the box of the block's u-th page
-                        const int shift = a.page_shift, rows = imin(kBN, 1 << shift), boxes = kBN / rows;
-                        const int pos = c0 + lane * rows, i0 = imax(p->i0, 0), i1 = p->i1;
-                        int page = -1;
-                        if (lane < boxes && pos < n_keys) {
-                            page = page_of(a.table + (size_t)p->b * a.max_pages, a.max_pages, a.num_pages, shift, pos);
-                            if (page < 0 && range_visible(i0, i1, pos, imin(pos + rows, n_keys) - 1, a.w, a.sinks))
-                                record_status(a.status, p->b, LF_ERR_BAD_PAGE);
+                        const int first_lane = j % (32 / boxes) * boxes, box = lane - first_lane;
+                        if (first_lane == 0) {
+                            page = next_page;
+                            pos = next_pos;
+                            look_up(j + 32 / boxes);
                         }
-                        const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+                        const bool mine = box >= 0 && box < boxes && page >= 0;
+                        const unsigned have = __ballot_sync(0xffffffffu, mine) >> first_lane;
                         ok = warp_wait(&kv_empty[s], ((g / kStages) & 1) ^ 1, abort_flag);
                         if (!ok) break;
                         if (lane == 0) {
@@ -306,17 +322,17 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                             for (int u = 0; u < boxes; ++u)
                                 if ((have >> u) & 1) m |= low_bits64(rows) << (u * rows);
                             // and only keys some row sees: others' values may be anything
-                            valid[s] = m & low_bits64(imin(n_keys, i1 + 1) - c0) &
-                                       (~low_bits64(i0 - a.w - c0) | low_bits64(a.sinks - c0));
+                            valid[s] = m & low_bits64(imin(n_keys, p->i1 + 1) - c0) &
+                                       (~low_bits64(imax(p->i0, 0) - a.w - c0) | low_bits64(a.sinks - c0));
                             const uint32_t bytes = __popc(have) * rows * kD * 2;
                             if (bytes) mbar_arrive_expect_tx(&kv_full[s], 2 * bytes);
                             else mbar_arrive(&kv_full[s]);
                         }
                         __syncwarp();
-                        if (page >= 0) {
-                            const int slot = pos & ((1 << shift) - 1);
-                            tma_load_4d(ks + lane * rows * kD * 2, &maps.k, &kv_full[s], 0, hk, slot, page);
-                            tma_load_4d(vs + lane * rows * kD * 2, &maps.v, &kv_full[s], 0, hk, slot, page);
+                        if (mine) {
+                            const int slot = pos & ((1 << a.page_shift) - 1);
+                            tma_load_4d(ks + box * rows * kD * 2, &maps.k, &kv_full[s], 0, hk, slot, page);
+                            tma_load_4d(vs + box * rows * kD * 2, &maps.v, &kv_full[s], 0, hk, slot, page);
                         }
                         __syncwarp();
                     } else {
@@ -333,16 +349,16 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             }
             if (!ok && lane == 0) {  // wind-down: let issued copies land
                 volatile int never = 0;
-                for (int c = it > 2 ? it - 2 : 0; c < it; ++c) mbar_wait(&q_full[c & 1], (c >> 1) & 1, &never, 200000000ull);
+                if (it > 0) mbar_wait(q_full, (it - 1) & 1, &never, 200000000ull);
                 for (int c = g > kStages ? g - kStages : 0; c < g; ++c)
                     mbar_wait(&kv_full[c % kStages], (c / kStages) & 1, &never, 200000000ull);
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMA
-            // In issue order S_0, S_1, PV_0, S_2, PV_1, ...: the products run
-            // in that order, so S of block g + 1 may overwrite P of block
-            // g - 1 without a wait.  The first PV of a tile overwrites O: it
-            // waits for the P of warps that have read the last tile's O.
+            // In issue order S_0, PV_0, S_1, PV_1, ...: the products run in
+            // that order, so S of a block may overwrite P of the one before
+            // without a wait.  The first PV of a tile overwrites O: it waits
+            // for the P of warps that have read the last tile's O.
             constexpr uint32_t id_s = idesc_f16(MmaFormat<T>::fmt, kBM, kBN, 0, 0);
             constexpr uint32_t id_o = idesc_f16(MmaFormat<T>::fmt, kBM, kD, 0, 1);
             const uint64_t dq = desc_sw128(smem_u32(smem)), dk = desc_sw128(smem_u32(smem + kOffK)),
@@ -357,26 +373,19 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 }
                 const int nb = p->nb;
                 if (nb == 0) continue;
-                auto scores = [&](int j) -> bool {
-                    const int s = (g + j) % kStages, buf = (g + j) & 1;
-                    if (!warp_wait(&kv_full[s], ((g + j) / kStages) & 1, abort_flag)) return false;
-                    tc_fence_after();
-                    mma4_ss(tmem + buf * kBN, dq + (it & 1) * (kQBytes >> 4), dk + s * (kKBytes >> 4), id_s);
-                    commit_elect(&s_full[buf]);
-                    if (j == nb - 1) commit_elect(&q_empty[it & 1]);
-                    return true;
-                };
-                ok = warp_wait(&q_full[it & 1], (it >> 1) & 1, abort_flag) && scores(0);
+                ok = warp_wait(q_full, it & 1, abort_flag);
                 for (int j = 0; j < nb && ok; ++j) {
                     const int c = g + j, s = c % kStages;
-                    // S of block j + 1 reuses the buffer of P of j - 1: its PV has been issued
-                    if (j + 1 < nb) ok = scores(j + 1);
-                    ok = ok && warp_wait(&p_full[c & 1], (c >> 1) & 1, abort_flag);
+                    ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    // half 0's keys into its O, half 1's into the other
-                    mma4_ts(tmem + kTmemO, tmem + kTmemO + kD, tmem + (c & 1) * kBN, dv + s * (kKBytes >> 4), id_o, j > 0,
-                            j > 0);
+                    mma4_ss(tmem, dq, dk + s * (kKBytes >> 4), id_s);
+                    commit_elect(s_full);
+                    if (j == nb - 1) commit_elect(q_empty);
+                    ok = warp_wait(p_full, c & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma4_ts<16>(tmem + kTmemO, tmem + kTmemO, tmem, dv + s * (kKBytes >> 4), id_o, j > 0, 1);
                     commit_elect(&kv_empty[s]);
                     if (j == nb - 1) commit_elect(o_full);
                 }
@@ -392,12 +401,11 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     } else {
         // ------------------------------------------------------------ softmax
         regs_inc<kRegsSoftmax>();
-        // this thread's row of a tile and its half of the keys
-        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        // this thread's row of a tile
+        const int r = threadIdx.x;
         const int r_tok = r / G, r_head = r % G;
         const bool row_used = r < TQ * G;
-        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tO = t_lane + kTmemO + half * kD;
+        const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16), tO = tS + kTmemO;
         const float sc = a.scale * kLog2e;
         bool ok = true;
         int g = 0, it = 0;
@@ -408,7 +416,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             const bool row_stored = row_used && tok < p->rows;
             const int i = row_used && tok < p->n ? p->first + tok : -1;  // this row's position
             if (nb == 0) {
-                if (half == 0 && row_stored) {
+                if (row_stored) {
                     const size_t orow = ((size_t)p->batch * L + p->start + tok) * a.Hq + p->hk * G + r_head;
                     zero_row64(static_cast<T*>(a.out) + orow * kD);
                     if constexpr (!kPaged)
@@ -421,13 +429,13 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < nb; ++j) {
                 const int c = g + j, s = c % kStages, c0 = p->key0(j);
-                const uint32_t tS = t_lane + (c & 1) * kBN + half * 32;
                 bool full = c0 <= full_hi && c0 >= full_lo;
-                ok = warp_wait(&s_full[c & 1], (c >> 1) & 1, abort_flag);
+                ok = warp_wait(s_full, c & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                float x[32];
+                float x[kBN];
                 tmem_ld32f(tS, x);
+                tmem_ld32f(tS + 32, x + 32);
                 unsigned long long have = ~0ull;  // keys that exist (and, paged, that some row sees)
                 if constexpr (kPaged) {
                     // (published before the loads of the stage were issued)
@@ -439,16 +447,19 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     have = low_bits64(n_keys - c0);
                 }
                 tmem_ld_wait();
-                regs_ready<32>(x);
+                regs_ready<kBN>(x);
                 if (!full) {
-                    const uint32_t bits =
-                        visible_bits32(i, c0 + half * 32, n_keys, a.w, a.sinks) & (uint32_t)(have >> (32 * half));
+                    const uint32_t lo = visible_bits32(i, c0, n_keys, a.w, a.sinks) & (uint32_t)have;
+                    const uint32_t hi = visible_bits32(i, c0 + 32, n_keys, a.w, a.sinks) & (uint32_t)(have >> 32);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1 ? x[e] : -INFINITY;
+                    for (int e = 0; e < 32; ++e) {
+                        x[e] = (lo >> e) & 1 ? x[e] : -INFINITY;
+                        x[e + 32] = (hi >> e) & 1 ? x[e + 32] : -INFINITY;
+                    }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < kBN; e += 8) {
                     mx[0] = max3(mx[0], x[e], x[e + 1]);
                     mx[1] = max3(mx[1], x[e + 2], x[e + 3]);
                     mx[2] = max3(mx[2], x[e + 4], x[e + 5]);
@@ -456,106 +467,95 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 }
                 const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 const bool need = cm > m + kRescale || (m == -INFINITY && cm > m);
-                if (__any_sync(0xffffffffu, need)) {
-                    const bool real = need && m != -INFINITY;
-                    if (__any_sync(0xffffffffu, real)) {
-                        // the products into O must be done: the last one
-                        // releases its stage (and none follows without this
-                        // warp's P)
-                        ok = warp_wait(&kv_empty[(c - 1) % kStages], ((c - 1) / kStages) & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const float f = real ? ex2(m - cm) : 1.0f;
-                        l *= f;
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            float o[16];
-                            tmem_ld16f(tO + h * 16, o);
-                            tmem_ld_wait();
-                            regs_ready<16>(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            tmem_st16f(tO + h * 16, o);
-                        }
-                    }
-                    if (need) m = cm;
+                float f = 1.0f;
+                bool real = false;
+                if (need) {
+                    real = m != -INFINITY;
+                    f = real ? ex2(m - cm) : 1.0f;
+                    m = cm;
+                    l *= f;
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;
                 const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 v = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc2, nm2);
-                    const float2 q = make_float2(ex2(v.x), ex2(v.y));
-                    sum[e & 1] = fadd2(sum[e & 1], q);
-                    pk[e] = Pair<T>::pack(q.x, q.y);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 v = ffma2(make_float2(x[32 * h + 2 * e], x[32 * h + 2 * e + 1]), sc2, nm2);
+                        const float2 q = make_float2(ex2(v.x), ex2(v.y));
+                        sum[e & 1] = fadd2(sum[e & 1], q);
+                        pk[e] = Pair<T>::pack(q.x, q.y);
+                    }
+                    tmem_st16(tS + h * 16, pk);
                 }
-                tmem_st16(tS, pk);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                if (__any_sync(0xffffffffu, real)) {
+                    // (S of this block is done, and with it every earlier
+                    // product into O)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        float o[16];
+                        tmem_ld16f(tO + h * 16, o);
+                        tmem_ld_wait();
+                        regs_ready<16>(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tmem_st16f(tO + h * 16, o);
+                    }
+                }
                 if (have != ~0ull) {
                     // rows of V that are no key of the sequence: 0 * NaN is NaN
                     ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
                     if (!ok) break;
-                    const int row = threadIdx.x >> 2;
+                    const int row = threadIdx.x >> 1;
                     if (!((have >> row) & 1)) {
-                        uint4* zr = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 3) * 32);
-                        zr[0] = zr[1] = make_uint4(0u, 0u, 0u, 0u);
+                        uint4* zr = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 1) * 64);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) zr[u] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[c & 1]);
+                if (lane == 0) mbar_arrive(p_full);
             }
             if (ok) ok = warp_wait(o_full, it & 1, abort_flag);
-            if (ok) {  // join the halves
-                ml[half * kBM + r] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ml_full);
-                ok = warp_wait(ml_full, it & 1, abort_flag);
-            }
             if (ok) {
                 tc_fence_after();
-                const float2 u0 = ml[r], u1 = ml[kBM + r];
-                const float top = fmaxf(u0.x, u1.x), base = top == -INFINITY ? 0.0f : top;
-                const float f0 = ex2(u0.x - base), f1 = ex2(u1.x - base), sum = u0.y * f0 + u1.y * f1;
-                const bool none = i < 0 || sum == 0.0f;  // no token of the sequence, or no key
-                const float inv = rcp_approx(sum), lse2 = none ? -INFINITY : top + lg2_approx(sum);
+                const bool none = i < 0 || l == 0.0f;  // no token of the sequence, or no key
+                const float inv = rcp_approx(l), lse2 = none ? -INFINITY : m + lg2_approx(l);
                 const size_t orow = ((size_t)p->batch * L + p->start + tok) * a.Hq + p->hk * G + r_head;
-                float o[32], o1[32];
-                tmem_ld32f(t_lane + kTmemO + half * 32, o);
-                tmem_ld32f(t_lane + kTmemO + kD + half * 32, o1);
-                tmem_ld_wait();
-                regs_ready<32>(o);
-                regs_ready<32>(o1);
-                tc_fence_before();
-                const float2 g0 = make_float2(f0 * inv, f0 * inv), g1 = make_float2(f1 * inv, f1 * inv);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 v = ffma2(make_float2(o[e], o[e + 1]), g0, fmul2(make_float2(o1[e], o1[e + 1]), g1));
-                    o[e] = v.x;
-                    o[e + 1] = v.y;
-                }
-                if (none) {
+                for (int h = 0; h < 2; ++h) {
+                    float o[32];
+                    tmem_ld32f(tO + h * 32, o);
+                    tmem_ld_wait();
+                    regs_ready<32>(o);
+                    if (h == 1) tc_fence_before();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-                }
-                if (row_stored) {
-                    if (kPaged && p->part) {
-                        const size_t at = (size_t)p->z * ((size_t)L * a.Hq) + orow;
-                        float4* d = reinterpret_cast<float4*>(pp.o + at * kD + half * 32);
+                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                    if (none) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        if (half == 0) pp.lse[at] = lse2;
-                    } else {
-                        store_row32(static_cast<T*>(a.out) + orow * kD + half * 32, o);
-                        if constexpr (!kPaged) {
-                            if (half == 0)
-                                a.lse[((size_t)p->batch * a.Hq + p->hk * G + r_head) * L + p->start + tok] = lse2 * kLn2;
+                        for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                    }
+                    if (row_stored) {
+                        if (kPaged && p->part) {
+                            float4* d = reinterpret_cast<float4*>(pp.o + ((size_t)p->z * ((size_t)L * a.Hq) + orow) * kD + h * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        } else {
+                            store_row32(static_cast<T*>(a.out) + orow * kD + h * 32, o);
                         }
                     }
+                    __syncwarp();
+                }
+                if (row_stored) {
+                    if (kPaged && p->part) pp.lse[(size_t)p->z * ((size_t)L * a.Hq) + orow] = lse2;
+                    if constexpr (!kPaged)
+                        a.lse[((size_t)p->batch * a.Hq + p->hk * G + r_head) * L + p->start + tok] = lse2 * kLn2;
                 }
                 __syncwarp();
             }
