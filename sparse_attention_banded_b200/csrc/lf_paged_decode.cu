@@ -252,26 +252,24 @@ decode_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Paged
     }
 }
 
-// Partials of one row: the weighted sum of some of them.
+// Partials of one row: the weighted sum of some of them, 4 elements a lane.
 struct Joined {
     float top, sum;
-    float2 x;  // elements 2 lane, 2 lane + 1
+    float4 x;
 };
-// `count` partials `step` rows apart, every `stride`-th from `from` on.
+// `count` partials `step` rows apart, every `stride`-th from `from` on; o:
+// this lane's elements of the first.
 __device__ __forceinline__ Joined join(const float* o, const float* e, size_t step, int count, int from, int stride) {
-    const int lane = threadIdx.x & 31;
-    Joined j = {-INFINITY, 0.f, make_float2(0.f, 0.f)};
-    for (int s = from + lane * stride; s < count; s += 32 * stride) j.top = fmaxf(j.top, e[s * step]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) j.top = fmaxf(j.top, __shfl_xor_sync(0xffffffffu, j.top, d));
+    Joined j = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int s = from; s < count; s += stride) j.top = fmaxf(j.top, e[s * step]);
     const float base = j.top == -INFINITY ? 0.f : j.top;
-#pragma unroll 8
+#pragma unroll 4
     for (int s = from; s < count; s += stride) {
         const float f = ex2(e[s * step] - base);
-        const float2 v = *reinterpret_cast<const float2*>(o + s * step * kD + 2 * lane);
+        const float4 v = *reinterpret_cast<const float4*>(o + s * step * kD);
         j.sum += f;
-        j.x.x = fmaf(f, v.x, j.x.x);
-        j.x.y = fmaf(f, v.y, j.x.y);
+        j.x = make_float4(fmaf(f, v.x, j.x.x), fmaf(f, v.y, j.x.y), fmaf(f, v.z, j.x.z), fmaf(f, v.w, j.x.w));
     }
     return j;
 }
@@ -280,23 +278,24 @@ __device__ __forceinline__ Joined join2(const Joined& a, const Joined& b) {
     j.top = fmaxf(a.top, b.top);
     const float base = j.top == -INFINITY ? 0.f : j.top, fa = ex2(a.top - base), fb = ex2(b.top - base);
     j.sum = a.sum * fa + b.sum * fb;
-    j.x = make_float2(a.x.x * fa + b.x.x * fb, a.x.y * fa + b.x.y * fb);
+    j.x = make_float4(a.x.x * fa + b.x.x * fb, a.x.y * fa + b.x.y * fb, a.x.z * fa + b.x.z * fb, a.x.w * fa + b.x.w * fb);
     return j;
 }
 
-// Joins the pieces of rows that have several.  kPerRow of a block's 8 warps
-// share a row (all of them where a context may be cut into many pieces), or
-// one warp takes kRowsEach rows (heads) of a token, looking its sequence up once.
-template <typename T, int kPerRow, int kRowsEach>
+// Joins the pieces of rows that have several, half a warp per row.  kBlock:
+// the 16 half warps of a block share one row (a context may be cut into many
+// pieces); else a warp takes kEach heads of one token, two at a time, and
+// looks its sequence up once.
+template <typename T, bool kBlock, int kEach>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedPlan pl) {
-    __shared__ Joined parts[8][32];
+    __shared__ Joined parts[16][16];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPerRow;
-    const int each = (a.Hq + kRowsEach - 1) / kRowsEach;  // warps (or blocks) per token
-    const long long at = (long long)blockIdx.x * (8 / kPerRow) + warp / kPerRow;
+    const int lane = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1, G = a.Hq / a.Hkv;
+    const int each = (a.Hq + kEach - 1) / kEach;  // warps (blocks) per token
+    const long long at = kBlock ? blockIdx.x : (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (at >= (long long)a.T * each) return;
-    const int tok = (int)(at / each), h0 = (int)(at % each) * kRowsEach, G = a.Hq / a.Hkv;
+    const int tok = (int)(at / each), h0 = (int)(at % each) * kEach;
     const int b = seq_of_token_warp(a.cu, a.n_seqs, tok);
     const int start = iclamp(a.cu[b], 0, a.T), n = iclamp(a.cu[b + 1], 0, a.T) - start;
     if (tok < start || tok >= start + n) return;
@@ -310,20 +309,25 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
         pieces = (tile_key_blocks(first, t0, imin(t0 + TQ, n), kv, a.w, a.sinks).n + pl.per - 1) / pl.per;
     }
     if (pieces <= 1) return;  // written whole
-#pragma unroll 4
-    for (int h = h0; h < imin(h0 + kRowsEach, a.Hq); ++h) {
-        const size_t row = (size_t)tok * a.Hq + h;
-        Joined j = join(pl.o + row * kD, pl.lse + row, (size_t)a.T * a.Hq, pieces, part, kPerRow);
-        if constexpr (kPerRow > 1) {
-            static_assert(kPerRow == 8 && kRowsEach == 1, "one row per block");
-            parts[warp][lane] = j;
-            __syncthreads();
-            if (warp > 0) return;
-#pragma unroll
-            for (int u = 1; u < 8; ++u) j = join2(j, parts[u][lane]);
-        }
+    const size_t step = (size_t)a.T * a.Hq, row0 = (size_t)tok * a.Hq + h0;
+    auto store = [&](const Joined& j, size_t row) {
         const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
-        reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * kD)[lane] = Pair<T>::pack(j.x.x * inv, j.x.y * inv);
+        reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * kD)[lane] =
+            make_uint2(Pair<T>::pack(j.x.x * inv, j.x.y * inv), Pair<T>::pack(j.x.z * inv, j.x.w * inv));
+    };
+    if constexpr (kBlock) {
+        static_assert(kEach == 1, "one row per block");
+        const int part = threadIdx.x >> 4;
+        parts[part][lane] = join(pl.o + row0 * kD + 4 * lane, pl.lse + row0, step, pieces, part, 16);
+        __syncthreads();
+        if (part > 0) return;
+        Joined j = parts[0][lane];
+        for (int u = 1; u < 16; ++u) j = join2(j, parts[u][lane]);
+        store(j, row0);
+    } else {
+#pragma unroll
+        for (int h = half; h < kEach; h += 2)
+            if (h0 + h < a.Hq) store(join(pl.o + (row0 + h) * kD + 4 * lane, pl.lse + row0 + h, step, pieces, 0, 1), row0 + h);
     }
 }
 
@@ -337,15 +341,14 @@ lf_status paged_t(const PagedArgs& a, const PagedPlan& pl, cudaStream_t stream) 
     if (st != LF_OK || pl.splits() <= 1) return st;
     // A block per row for more than 16 pieces and no more blocks than run at
     // once (98 pieces of one context of 100000: 80 us by a warp per row, 23
-    // by a block); eight rows a warp where there are more rows than warps
-    // (24 us by a warp each for 32768 rows).
+    // by a block); eight heads a warp where there are more rows than half
+    // warps (32768 rows of two pieces: 22 us by a warp per row).
     const long long rows = (long long)a.T * a.Hq;
+    auto warps = [&](int each) { return dim3((unsigned)(((long long)a.T * ((a.Hq + each - 1) / each) + 7) / 8)); };
     if (pl.splits() > 16 && rows <= 8 * 148)
-        return launch_pdl(merge_kernel<T, 8, 1>, dim3((unsigned)rows), dim3(256), 0, stream, a, pl);
-    if (rows <= 64 * 148)
-        return launch_pdl(merge_kernel<T, 1, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, a, pl);
-    const long long warps = (long long)a.T * ((a.Hq + 7) / 8);
-    return launch_pdl(merge_kernel<T, 1, 8>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, a, pl);
+        return launch_pdl(merge_kernel<T, true, 1>, dim3((unsigned)rows), dim3(256), 0, stream, a, pl);
+    if (rows <= 128 * 148) return launch_pdl(merge_kernel<T, false, 2>, warps(2), dim3(256), 0, stream, a, pl);
+    return launch_pdl(merge_kernel<T, false, 8>, warps(8), dim3(256), 0, stream, a, pl);
 }
 
 }  // namespace
