@@ -61,17 +61,19 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
         p.decode_splits = (int)((tiles + p.chunk - 1) / p.chunk);
     }
     if (p.tensor) {
-        // Rounds of the 4 x 148 resident CTAs times blocks per item; pieces
-        // are joined by a further kernel, worth about 12 blocks (3 when it
-        // runs anyway, for the decode kernel).  Next to single tokens, which
-        // are no tiles, a quarter of the sequences are taken to end in one.
-        const int join = p.decode && p.decode_splits > 1 ? 3 : 12;
+        // In units of 0.1 us: up to 296 items run at once (two per SM, worked
+        // on ahead), a block in 8; of more, 592 run at a time (four per SM),
+        // a block in 22.  Pieces are joined by a further kernel, worth 80 (10
+        // when it runs anyway, for the decode kernel).  Next to single tokens, which are no tiles, a quarter of
+        // the sequences are taken to end in one.
+        const int join = p.decode && p.decode_splits > 1 ? 10 : 80;
         const long long blocks = most_blocks(max_q, width, w, sinks, 64);
         const long long tiles = ((long long)T / (128 / G) + (p.decode ? (n_seqs + 3) / 4 : n_seqs)) * Hkv;
         long long best = -1;
         for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
-            const long long per = (blocks + s - 1) / s, rounds = (tiles * s + 591) / 592;
-            const long long cost = rounds * (per + 2) + (s > 1 ? join : 0);
+            const long long per = (blocks + s - 1) / s, items = tiles * s;
+            const long long cost =
+                (items <= 296 ? (per + 2) * 8 : (items + 591) / 592 * (per + 2) * 22) + (s > 1 ? join : 0);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.per = (int)per;

@@ -8,16 +8,19 @@
 //     S = Q K^T                        (tcgen05.mma, fp32 in tensor memory)
 //     m' = max(m, max s), P = 2^(s - m'), l += sum P
 //     O = O 2^(m - m') + P V           (P from tensor memory)
-// One thread per row; P overwrites the first half of S's columns.  S and O
-// take 128 tensor-memory columns: four CTAs per SM.  A CTA's block is a chain
-// of latencies (product, softmax, product, 2500 cycles of which the
-// arithmetic is a third), and the four chains fill each other's gaps.  (Two
-// threads a row with the next S under this softmax, two CTAs per SM: 70 us
-// instead of 59 for 4 x 4096 tokens, 16 heads, window 256.)  A tile of its
-// own launch paid 8000 cycles more to start and end, so CTAs are persistent
-// and the loads and plan of the next tile run under the end of this one.
-// The four softmax warps keep 64 scores a row in registers, of the share
-// that the other warps give up.
+// One thread per row; P overwrites the first half of S's columns.  A CTA's
+// block is a chain of latencies (product, softmax, product: 2500 cycles, of
+// which the arithmetic is a third).  Many tiles: S and O take 128
+// tensor-memory columns, four CTAs per SM, and their chains fill each other's
+// gaps.  (4 x 4096 tokens, 16 heads, window 256: 59 us, and 70 with two CTAs
+// per SM and two threads a row.)  Few tiles: two CTAs per SM with two buffers
+// of S, and the next block's S runs under this one's softmax (two chunks of
+// 1024 tokens, 16 / 4 heads, window 4096, 264 items: 78 us with the append,
+// and 104 the other way).
+// A tile of its own launch paid 8000 cycles more to start and end, so CTAs
+// are persistent and the loads and plan of the next tile run under the end of
+// this one.  The four softmax warps keep 64 scores a row in registers, of the
+// share that the other warps give up.
 // The O update is skipped unless a row's maximum grows by more than 2^8 (P
 // <= 2^8 then).  P is rounded to the storage type, the MMA's operand type;
 // sums stay fp32.
@@ -77,27 +80,38 @@ using namespace sm100;
 constexpr int kBM = 128;   // query rows
 constexpr int kBN = 64;    // keys per block
 constexpr int kD = 64;
-constexpr int kStages = 2;
 constexpr int kRing = 4;   // plans ahead
 constexpr int kSoftmaxWarps = 4;
 constexpr int kTmaWarp = 4, kMmaWarp = 5, kPlanWarp = 6;
 constexpr int kThreads = 8 * 32;
-constexpr int kCtas = 4;   // per SM
-// 64 registers a thread at launch; a block's share is split anew.
-constexpr uint32_t kRegsLaunch = 64, kRegsProducer = 24, kRegsSoftmax = 104;
-static_assert(4 * 32 * kRegsProducer + 4 * 32 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kQBytes = kBM * kD * 2, kKBytes = kBN * kD * 2;
-constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffPlan = kOffV + kStages * kKBytes;
 constexpr uint32_t kPlanBytes = 80;
-constexpr uint32_t kOffBar = kOffPlan + kRing * kPlanBytes;
-constexpr uint32_t kBars = 2 + 2 * kStages + 4 + 2 * kRing;
-constexpr uint32_t kOffMask = kOffBar + kBars * 8;               // valid keys of each stage (paged)
-constexpr uint32_t kOffMisc = kOffMask + kStages * 8;
-constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;            // + alignment slack
-constexpr uint32_t kTmemCols = 128, kTmemO = 64;                 // S (then P) at 0, O at 64
+
+// The two ways a CTA is laid out (the rule is at the launch).
+//   kAhead false: four CTAs per SM, each a chain of S, softmax, P V.
+//   kAhead true: two CTAs per SM, S double-buffered: the next block's S runs
+//   under this one's softmax, which shortens the chain of a lone CTA.
+template <bool kAhead>
+struct Layout {
+    static constexpr int kCtas = kAhead ? 2 : 4;  // per SM
+    static constexpr int kStages = kAhead ? 4 : 2;
+    static constexpr int kBufs = kAhead ? 2 : 1;  // of S
+    // Registers a thread at launch; a block's share is split anew.
+    static constexpr uint32_t kRegsLaunch = kAhead ? 128 : 64, kRegsProducer = kAhead ? 96 : 24,
+                              kRegsSoftmax = kAhead ? 160 : 104;
+    static_assert(4 * 32 * kRegsProducer + 4 * 32 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+    static constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffPlan = kOffV + kStages * kKBytes;
+    static constexpr uint32_t kOffBar = kOffPlan + kRing * kPlanBytes;
+    static constexpr uint32_t kBars = 2 + 2 * kStages + 2 * kBufs + 2 + 2 * kRing;
+    static constexpr uint32_t kOffMask = kOffBar + kBars * 8;  // valid keys of each stage (paged)
+    static constexpr uint32_t kOffMisc = kOffMask + kStages * 8;
+    static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
+    static constexpr uint32_t kTmemCols = kAhead ? 256 : 128, kTmemO = kBufs * kBN;  // S (then P) before O
+    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
+};
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
-static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "CTAs per SM");
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -171,33 +185,38 @@ __device__ bool make_plan(const A& a, const PagedPlan& pp, int item, Plan& p, bo
     return true;
 }
 
-template <typename T, bool kPaged, typename A>
-__global__ void __launch_bounds__(kThreads, kCtas)
+template <typename T, bool kPaged, bool kAhead, typename A>
+__global__ void __launch_bounds__(kThreads, Layout<kAhead>::kCtas)
 window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, const __grid_constant__ PagedPlan pp,
               int n_items) {
+    using Lay = Layout<kAhead>;
+    constexpr int kStages = Lay::kStages, kBufs = Lay::kBufs;
+    constexpr uint32_t kOffK = Lay::kOffK, kOffV = Lay::kOffV, kOffPlan = Lay::kOffPlan, kTmemO = Lay::kTmemO;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBar);
     uint64_t* q_empty = q_full + 1;
     uint64_t* kv_full = q_empty + 1;
     uint64_t* kv_empty = kv_full + kStages;
-    uint64_t* s_full = kv_empty + kStages;
-    uint64_t* p_full = s_full + 1;
-    uint64_t* o_full = p_full + 1;
+    uint64_t* s_full = kv_empty + kStages;  // [kBufs], as the next
+    uint64_t* p_full = s_full + kBufs;
+    uint64_t* o_full = p_full + kBufs;
     uint64_t* drain = o_full + 1;
     uint64_t* plan_full = drain + 1;
     uint64_t* plan_empty = plan_full + kRing;
-    volatile unsigned long long* valid = reinterpret_cast<volatile unsigned long long*>(smem + kOffMask);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+    volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + Lay::kOffMask);  // [stage][2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kOffMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        mbar_init(s_full, 1);
-        mbar_init(p_full, kSoftmaxWarps);
+        for (int u = 0; u < kBufs; ++u) {
+            mbar_init(&s_full[u], 1);
+            mbar_init(&p_full[u], kSoftmaxWarps);
+        }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
@@ -219,7 +238,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     // (only now: a kernel that runs before may hold tensor memory until it ends)
     pdl_wait();
     if (warp == kMmaWarp) {
-        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_alloc(tmem_slot, Lay::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -240,7 +259,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     };
 
     if (warp >= kSoftmaxWarps) {
-        regs_dec<kRegsProducer>();
+        regs_dec<Lay::kRegsProducer>();
         if (warp == kPlanWarp) {
             // -------------------------------------------------------- plans
             const int32_t* lens = nullptr;
@@ -322,8 +341,10 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                             for (int u = 0; u < boxes; ++u)
                                 if ((have >> u) & 1) m |= low_bits64(rows) << (u * rows);
                             // and only keys some row sees: others' values may be anything
-                            valid[s] = m & low_bits64(imin(n_keys, p->i1 + 1) - c0) &
-                                       (~low_bits64(imax(p->i0, 0) - a.w - c0) | low_bits64(a.sinks - c0));
+                            m &= low_bits64(imin(n_keys, p->i1 + 1) - c0) &
+                                 (~low_bits64(imax(p->i0, 0) - a.w - c0) | low_bits64(a.sinks - c0));
+                            valid[2 * s] = (uint32_t)m;
+                            valid[2 * s + 1] = (uint32_t)(m >> 32);
                             const uint32_t bytes = __popc(have) * rows * kD * 2;
                             if (bytes) mbar_arrive_expect_tx(&kv_full[s], 2 * bytes);
                             else mbar_arrive(&kv_full[s]);
@@ -355,10 +376,11 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             }
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- MMA
-            // In issue order S_0, PV_0, S_1, PV_1, ...: the products run in
-            // that order, so S of a block may overwrite P of the one before
-            // without a wait.  The first PV of a tile overwrites O: it waits
-            // for the P of warps that have read the last tile's O.
+            // In issue order S_0, PV_0, S_1, PV_1, ... (or, ahead, S_0, S_1,
+            // PV_0, S_2, PV_1, ...): the products run in that order, so S of
+            // a block may overwrite P of the last one in its buffer without a
+            // wait.  The first PV of a tile overwrites O: it waits for the P
+            // of warps that have read the last tile's O.
             constexpr uint32_t id_s = idesc_f16(MmaFormat<T>::fmt, kBM, kBN, 0, 0);
             constexpr uint32_t id_o = idesc_f16(MmaFormat<T>::fmt, kBM, kD, 0, 1);
             const uint64_t dq = desc_sw128(smem_u32(smem)), dk = desc_sw128(smem_u32(smem + kOffK)),
@@ -373,19 +395,26 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 }
                 const int nb = p->nb;
                 if (nb == 0) continue;
+                auto scores = [&](int j) -> bool {
+                    const int c = g + j, s = c % kStages;
+                    if (!warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag)) return false;
+                    tc_fence_after();
+                    mma4_ss(tmem + c % kBufs * kBN, dq, dk + s * (kKBytes >> 4), id_s);
+                    commit_elect(&s_full[c % kBufs]);
+                    if (j == nb - 1) commit_elect(q_empty);
+                    return true;
+                };
                 ok = warp_wait(q_full, it & 1, abort_flag);
+                if (kAhead) ok = ok && scores(0);
                 for (int j = 0; j < nb && ok; ++j) {
                     const int c = g + j, s = c % kStages;
-                    ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
+                    if (!kAhead) ok = scores(j);
+                    else if (j + 1 < nb) ok = scores(j + 1);
+                    ok = ok && warp_wait(&p_full[c % kBufs], (c / kBufs) & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    mma4_ss(tmem, dq, dk + s * (kKBytes >> 4), id_s);
-                    commit_elect(s_full);
-                    if (j == nb - 1) commit_elect(q_empty);
-                    ok = warp_wait(p_full, c & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma4_ts<16>(tmem + kTmemO, tmem + kTmemO, tmem, dv + s * (kKBytes >> 4), id_o, j > 0, 1);
+                    mma4_ts<16>(tmem + kTmemO, tmem + kTmemO, tmem + c % kBufs * kBN, dv + s * (kKBytes >> 4), id_o,
+                                j > 0, 1);
                     commit_elect(&kv_empty[s]);
                     if (j == nb - 1) commit_elect(o_full);
                 }
@@ -400,12 +429,12 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
         }
     } else {
         // ------------------------------------------------------------ softmax
-        regs_inc<kRegsSoftmax>();
+        regs_inc<Lay::kRegsSoftmax>();
         // this thread's row of a tile
         const int r = threadIdx.x;
         const int r_tok = r / G, r_head = r % G;
         const bool row_used = r < TQ * G;
-        const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16), tO = tS + kTmemO;
+        const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16), tO = t_lane + kTmemO;
         const float sc = a.scale * kLog2e;
         bool ok = true;
         int g = 0, it = 0;
@@ -429,28 +458,31 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < nb; ++j) {
                 const int c = g + j, s = c % kStages, c0 = p->key0(j);
+                const uint32_t tS = t_lane + c % kBufs * kBN;
                 bool full = c0 <= full_hi && c0 >= full_lo;
-                ok = warp_wait(s_full, c & 1, abort_flag);
+                ok = warp_wait(&s_full[c % kBufs], (c / kBufs) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 float x[kBN];
                 tmem_ld32f(tS, x);
                 tmem_ld32f(tS + 32, x + 32);
-                unsigned long long have = ~0ull;  // keys that exist (and, paged, that some row sees)
+                bool all = c0 + kBN <= n_keys;  // every key exists (and, paged, some row sees it)
                 if constexpr (kPaged) {
                     // (published before the loads of the stage were issued)
                     ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
                     if (!ok) break;
-                    have = valid[s];
-                    full = full && have == ~0ull;
-                } else if (c0 + kBN > n_keys) {
-                    have = low_bits64(n_keys - c0);
+                    all = valid[2 * s] == ~0u && valid[2 * s + 1] == ~0u;
+                    full = full && all;
                 }
+                auto have = [&](int h) -> uint32_t {
+                    if constexpr (kPaged) return valid[2 * s + h];
+                    else return low_bits32(n_keys - c0 - 32 * h);
+                };
                 tmem_ld_wait();
                 regs_ready<kBN>(x);
                 if (!full) {
-                    const uint32_t lo = visible_bits32(i, c0, n_keys, a.w, a.sinks) & (uint32_t)have;
-                    const uint32_t hi = visible_bits32(i, c0 + 32, n_keys, a.w, a.sinks) & (uint32_t)(have >> 32);
+                    const uint32_t lo = visible_bits32(i, c0, n_keys, a.w, a.sinks) & have(0);
+                    const uint32_t hi = visible_bits32(i, c0 + 32, n_keys, a.w, a.sinks) & have(1);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         x[e] = (lo >> e) & 1 ? x[e] : -INFINITY;
@@ -492,8 +524,15 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 if (__any_sync(0xffffffffu, real)) {
-                    // (S of this block is done, and with it every earlier
-                    // product into O)
+                    // The products into O must be done.  They are, since S of
+                    // this block is, but for the last one where S runs ahead:
+                    // it releases its stage (and none follows without this
+                    // warp's P).
+                    if (kAhead) {
+                        ok = warp_wait(&kv_empty[(c - 1) % kStages], ((c - 1) / kStages) & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         float o[16];
@@ -505,12 +544,12 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                         tmem_st16f(tO + h * 16, o);
                     }
                 }
-                if (have != ~0ull) {
+                if (!all) {
                     // rows of V that are no key of the sequence: 0 * NaN is NaN
                     ok = warp_wait(&kv_full[s], (c / kStages) & 1, abort_flag);
                     if (!ok) break;
                     const int row = threadIdx.x >> 1;
-                    if (!((have >> row) & 1)) {
+                    if (!((have(row >> 5) >> (row & 31)) & 1)) {
                         uint4* zr = reinterpret_cast<uint4*>(smem + kOffV + s * kKBytes + row * 128 + (threadIdx.x & 1) * 64);
 #pragma unroll
                         for (int u = 0; u < 4; ++u) zr[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -520,7 +559,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
+                if (lane == 0) mbar_arrive(&p_full[c % kBufs]);
             }
             if (ok) ok = warp_wait(o_full, it & 1, abort_flag);
             if (ok) {
@@ -568,26 +607,35 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
     if (threadIdx.x == 0 && *abort_flag) record_status(a.status, 0, LF_ERR_DEVICE_TIMEOUT);
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, Lay::kTmemCols);
     }
 }
 
-template <typename T, bool kPaged, typename A>
-lf_status launch(const Maps& maps, const A& a, const PagedPlan& pp, long long items, cudaStream_t stream) {
+template <typename T, bool kPaged, bool kAhead, typename A>
+lf_status launch_as(const Maps& maps, const A& a, const PagedPlan& pp, int items, DeviceCtx* d, cudaStream_t stream) {
     static std::atomic<bool> attr[64];  // the shared-memory opt-in, per device
-    lf_status st;
-    DeviceCtx* d = current_device(&st);
-    if (!d) return st;
+    using Lay = Layout<kAhead>;
     if (!attr[d->ordinal].load()) {
-        if (cudaFuncSetAttribute(window_kernel<T, kPaged, A>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(window_kernel<T, kPaged, kAhead, A>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Lay::kSmemBytes) != cudaSuccess)
             return LF_ERR_CUDA;
         attr[d->ordinal].store(true);
     }
+    const int grid = imin(items, Lay::kCtas * d->sm_count);
+    return launch_pdl(window_kernel<T, kPaged, kAhead, A>, dim3(grid), dim3(kThreads), Lay::kSmemBytes, stream, maps, a, pp,
+                      items);
+}
+
+// Few tiles (at most two per SM) are worked on ahead: each is a chain of its
+// own.  More are worked on four per SM.
+template <typename T, bool kPaged, typename A>
+lf_status launch(const Maps& maps, const A& a, const PagedPlan& pp, long long items, cudaStream_t stream) {
+    lf_status st;
+    DeviceCtx* d = current_device(&st);
+    if (!d) return st;
     if (items > INT32_MAX / 2) return LF_ERR_TOO_LARGE;
-    const int grid = (int)(items < kCtas * d->sm_count ? items : kCtas * d->sm_count);
-    return launch_pdl(window_kernel<T, kPaged, A>, dim3(grid), dim3(kThreads), kSmemBytes, stream, maps, a, pp,
-                      (int)items);
+    return items <= 2 * d->sm_count ? launch_as<T, kPaged, true>(maps, a, pp, (int)items, d, stream)
+                                    : launch_as<T, kPaged, false>(maps, a, pp, (int)items, d, stream);
 }
 
 }  // namespace
