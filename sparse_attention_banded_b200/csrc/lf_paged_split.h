@@ -17,7 +17,8 @@ struct PagedPlan {
     int chunk;            // decode: tiles of 8 keys per CTA
     int decode_splits;    // pieces of a context (n_seqs times that: its gridDim.x)
     int per;              // tensor cores: blocks of 64 keys per CTA
-    int tensor_splits;    // its gridDim.z
+    int tensor_splits;    // pieces of a tile, at most
+    bool ahead;           // few items: two CTAs per SM, worked on ahead
     float* o;             // [splits][T * Hq][64]
     float* lse;           // [splits][T * Hq], log2
     LF_HD int splits() const { return imax(decode ? decode_splits : 1, tensor ? tensor_splits : 1); }
@@ -42,6 +43,12 @@ inline long long most_blocks(int max_q, int width, int w, int sinks, int bk) {
     return window < all ? window : all;
 }
 
+// Items of the tensor-core forward up to which each is worked on ahead, two
+// CTAs per SM; more run four per SM.  Both ways, 8 heads, window 2048: 128
+// items 29 and 39 us, 256 39 and 47, 320 41 and 54, 448 68 and 64, 2048 237
+// and 210; window 128: 256 12.4 and 14.4, 320 18.0 and 17.2, 2048 57 and 51.
+constexpr int kAheadItems = 2 * 148;
+
 // w and sinks clamped to the table's width.
 inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int width, int w, int sinks) {
     PagedPlan p = {};
@@ -64,8 +71,9 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
         // In units of 0.1 us: up to 296 items run at once (two per SM, worked
         // on ahead), a block in 8; of more, 592 run at a time (four per SM),
         // a block in 22.  Pieces are joined by a further kernel, worth 80 (10
-        // when it runs anyway, for the decode kernel).  Next to single tokens, which are no tiles, a quarter of
-        // the sequences are taken to end in one.
+        // when it runs anyway, for the decode kernel).  Next to single
+        // tokens, which are no tiles, a quarter of the sequences are taken to
+        // end in one.
         const int join = p.decode && p.decode_splits > 1 ? 10 : 80;
         const long long blocks = most_blocks(max_q, width, w, sinks, 64);
         const long long tiles = ((long long)T / (128 / G) + (p.decode ? (n_seqs + 3) / 4 : n_seqs)) * Hkv;
@@ -73,11 +81,12 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
         for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
             const long long per = (blocks + s - 1) / s, items = tiles * s;
             const long long cost =
-                (items <= 296 ? (per + 2) * 8 : (items + 591) / 592 * (per + 2) * 22) + (s > 1 ? join : 0);
+                (items <= kAheadItems ? (per + 2) * 8 : (items + 591) / 592 * (per + 2) * 22) + (s > 1 ? join : 0);
             if (best < 0 || cost < best) {
                 best = cost;
                 p.per = (int)per;
                 p.tensor_splits = (int)((blocks + per - 1) / per);
+                p.ahead = items <= kAheadItems;
             }
         }
     }

@@ -87,7 +87,7 @@ constexpr int kThreads = 8 * 32;
 constexpr uint32_t kQBytes = kBM * kD * 2, kKBytes = kBN * kD * 2;
 constexpr uint32_t kPlanBytes = 80;
 
-// The two ways a CTA is laid out (the rule is at the launch).
+// The two ways a CTA is laid out (the rule: kAheadItems).
 //   kAhead false: four CTAs per SM, each a chain of S, softmax, P V.
 //   kAhead true: two CTAs per SM, S double-buffered: the next block's S runs
 //   under this one's softmax, which shortens the chain of a lone CTA.
@@ -626,16 +626,14 @@ lf_status launch_as(const Maps& maps, const A& a, const PagedPlan& pp, int items
                       items);
 }
 
-// Few tiles (at most two per SM) are worked on ahead: each is a chain of its
-// own.  More are worked on four per SM.
 template <typename T, bool kPaged, typename A>
-lf_status launch(const Maps& maps, const A& a, const PagedPlan& pp, long long items, cudaStream_t stream) {
+lf_status launch(const Maps& maps, const A& a, const PagedPlan& pp, long long items, bool ahead, cudaStream_t stream) {
     lf_status st;
     DeviceCtx* d = current_device(&st);
     if (!d) return st;
     if (items > INT32_MAX / 2) return LF_ERR_TOO_LARGE;
-    return items <= 2 * d->sm_count ? launch_as<T, kPaged, true>(maps, a, pp, (int)items, d, stream)
-                                    : launch_as<T, kPaged, false>(maps, a, pp, (int)items, d, stream);
+    return ahead ? launch_as<T, kPaged, true>(maps, a, pp, (int)items, d, stream)
+                 : launch_as<T, kPaged, false>(maps, a, pp, (int)items, d, stream);
 }
 
 }  // namespace
@@ -648,8 +646,9 @@ lf_status launch_window_forward_tc(const WindowArgs& a, cudaStream_t stream) {
         return LF_ERR_CUDA;
     const PagedPlan pp = {};
     const long long items = (long long)token_slots(a.packed(), a.n_seqs, a.L, TQ) * a.Hkv;
-    if (a.dtype == LF_F16) return launch<__half, false>(maps, a, pp, items, stream);
-    return launch<__nv_bfloat16, false>(maps, a, pp, items, stream);
+    const bool ahead = items <= kAheadItems;
+    if (a.dtype == LF_F16) return launch<__half, false>(maps, a, pp, items, ahead, stream);
+    return launch<__nv_bfloat16, false>(maps, a, pp, items, ahead, stream);
 }
 
 lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& pp, cudaStream_t stream) {
@@ -660,8 +659,9 @@ lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& pp, cudaStream_t 
         !make_heads_map(&maps.v, a.v, a.Hkv, page, a.num_pages, 1, imin(page, kBN)))
         return LF_ERR_CUDA;
     const long long items = (long long)packed_slots(a.T, a.n_seqs, TQ) * a.Hkv * pp.tensor_splits;
-    if (a.dtype == LF_F16) return launch<__half, true>(maps, a, pp, items, stream);
-    return launch<__nv_bfloat16, true>(maps, a, pp, items, stream);
+    // (items counts slots, of which a batch of single tokens fills few)
+    if (a.dtype == LF_F16) return launch<__half, true>(maps, a, pp, items, pp.ahead, stream);
+    return launch<__nv_bfloat16, true>(maps, a, pp, items, pp.ahead, stream);
 }
 
 }  // namespace lf
