@@ -433,3 +433,16 @@ def test_one_context_in_many_pieces():
     Case([1], [40000], 2, 1, 64, seed=23).run().check()
     Case([1, 1], [40000, 30], 4, 1, 64, seed=24, w=30000, sinks=3).run().check()
     Case([1], [100], 4, 1, 64, seed=25, extra=1000).run().check()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("w,sinks", [(ALL, 0), (100, 4)])
+def test_more_chunks_than_the_gpu_holds(dtype, w, sinks):
+    """Equal chunks of many sequences, more tiles than two per SM."""
+    Case([17] * 90, [17 + (97 * i * i) % 700 for i in range(90)], 8, 4, 16, dtype, seed=w % 83, w=w, sinks=sinks).run().check()
+
+
+def test_many_ragged_chunks_next_to_single_tokens():
+    q = [1 + (7 * i * i) % 90 * (i % 2) for i in range(150)]
+    kv = [n + (53 * i) % 400 for i, n in enumerate(q)]
+    Case(q, kv, 10, 5, 32, "bf16", seed=9, w=300, sinks=2).run().check()

@@ -333,3 +333,37 @@ def test_heads_share_storage_with_the_output_of_a_projection():
     rows = lambda t: t.view(B, L, H, 64).transpose(1, 2)  # noqa: E731
     _compare([dict(out=rows(out)[b], lse=lse[b], dq=g[0][b], dk=g[1][b], dv=g[2][b]) for b in range(B)],
              [(q[b], k[b], v[b], rows(do)[b]) for b in range(B)], 40, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,w,sinks", [(6, 6, 30, 0), (9, 3, 20, 7), (12, 3, 1 << 30, 4), (6, 6, 0, 130)])
+def test_more_short_items_than_the_gpu_holds(dtype, Hq, Hkv, w, sinks):
+    """Hundreds of short sequences, empty and one-token ones among them: a
+    CTA takes several items, of which many hold nothing."""
+    lens = [(11 * i * i + 5 * i) % 37 * (i % 3) for i in range(300)]
+    _packed(lens[:100] + [290] + lens[100:], Hq, Hkv, w, sinks, dtype, seed=w % 89 + sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_more_padded_items_than_the_gpu_holds(dtype):
+    lens = [(13 * i * i + 7 * i) % 271 * (i % 2) for i in range(80)]
+    _padded(dtype, lens, 270, 8, 8, 50, 3, "blhd", seed=31)
+
+
+def test_a_captured_pass_of_many_items_repeats_bit_for_bit():
+    q, k, v, do = (_rand((2, 10, 6000, 64), "f16", 40 + s) for s in range(4))
+    do = do.transpose(1, 2).reshape(2, 6000, 640).contiguous()
+    out, lse = lf.lf_window_attention_forward(q, k, v, 64, 4)
+    want = lf.lf_window_attention_backward(q, k, v, out, lse, do, 64, 4)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, l = lf.lf_window_attention_forward(q, k, v, 64, 4)
+        got = lf.lf_window_attention_backward(q, k, v, o, l, do, 64, 4)
+    for _ in range(3):
+        for t in (o, l, *got):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, out) and torch.equal(l, lse)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
