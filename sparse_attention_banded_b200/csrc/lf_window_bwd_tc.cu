@@ -57,7 +57,7 @@ constexpr int kRing = 4;                                   // items ahead
 constexpr uint32_t kPlanBytes = 64;
 constexpr uint32_t kOffPlan = kOffRow + kRowFloats * 4;
 constexpr uint32_t kOffBar = kOffPlan + kRing * kPlanBytes;
-constexpr uint32_t kBars = 2 + 2 * kStages + 7 + 2 * kRing;
+constexpr uint32_t kBars = 2 + 2 * kStages + 8 + 2 * kRing;
 constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;      // + alignment slack
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
@@ -75,7 +75,7 @@ struct Maps {
 
 struct Ctx {
     uint8_t* smem;
-    uint64_t *a_full, *a_empty, *b_full, *b_empty, *s_full, *dp_full, *free_, *ready, *done, *drain, *plan_full, *plan_empty;
+    uint64_t *a_full, *a_empty, *b_full, *b_empty, *s_full, *dp_full, *free_, *ready, *done, *drain, *halves, *plan_full, *plan_empty;
     volatile int* abort_flag;
     uint32_t tmem;
 };
@@ -94,7 +94,8 @@ __device__ __forceinline__ Ctx setup(uint8_t* smem, int warp, int lane) {
     c.ready = c.free_ + 1;  // [2]
     c.done = c.ready + 2;
     c.drain = c.done + 1;
-    c.plan_full = c.drain + 1;
+    c.halves = c.drain + 1;
+    c.plan_full = c.halves + 1;
     c.plan_empty = c.plan_full + kRing;
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     c.abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
@@ -112,6 +113,7 @@ __device__ __forceinline__ Ctx setup(uint8_t* smem, int warp, int lane) {
         mbar_init(&c.ready[1], kMathWarps);
         mbar_init(c.done, 1);
         mbar_init(c.drain, 1);
+        mbar_init(c.halves, kMathWarps);
         for (int s = 0; s < kRing; ++s) {
             mbar_init(&c.plan_full[s], 1);
             mbar_init(&c.plan_empty[s], kMathWarps + 1);
@@ -180,6 +182,15 @@ __device__ __forceinline__ uint8_t* smem_base() {
 }
 
 // ---------------------------------------------------------------- dQ
+// delta comes from out as it was rounded to 16 bits, except where a row may
+// see few keys: there dP and delta nearly cancel, and the rounding would be
+// most of dS (window 1: errors of dQ and dK 2.3 times those of gradients
+// rounded once; a row that sees one key has none of either).  So a tile of
+// few blocks takes them twice, and the first pass sums delta = sum P dP in
+// fp32.  From four blocks on most rows see a hundred keys, and the 16-bit dS
+// is what is left (1.4 times).
+constexpr int kTwice = 3;
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
 dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs a) {
@@ -205,6 +216,8 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
     }
     const int i0 = t.t0, i1 = imin(t.t0 + TQ, t.n) - 1;
     const KeyBlocks kb = key_blocks(i0, i1, t.n, a.w, a.sinks, 64);
+    const int first = kb.n <= kTwice ? kb.n : 0, steps = first + kb.n;  // steps of the first pass, of both
+    auto key0 = [&](int j) { return key_block(kb, j < first ? j : j - first) * 64; };
     const Ctx c = setup(smem, warp, lane);
     const uint32_t tmS = c.tmem, tmP = c.tmem + 128, tmQ = c.tmem + 192;
     float* row_s = reinterpret_cast<float*>(smem + kOffRow);
@@ -218,13 +231,13 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
         }
         bool ok = true;
         int j = 0;
-        for (; j < kb.n; ++j) {
+        for (; j < steps; ++j) {
             const int s = j % kStages;
             ok = warp_wait(&c.b_empty[s], ((j / kStages) & 1) ^ 1, c.abort_flag);
             if (!ok) break;
             if (lane == 0) {
                 uint8_t* d = smem + kOffB + s * 2 * kSmall;
-                const int row = t.start + key_block(kb, j) * 64;
+                const int row = t.start + key0(j);
                 mbar_arrive_expect_tx(&c.b_full[s], 2 * kSmall);
                 tma_load_4d(d, &maps.k, &c.b_full[s], 0, hk, row, t.batch);
                 tma_load_4d(d + kSmall, &maps.v, &c.b_full[s], 0, hk, row, t.batch);
@@ -246,29 +259,31 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
             mma_nt<T>(tmS + (j & 1) * 64, smem_u32(smem), b0 + s * 2 * kSmall);
             mma_nt<T>(tmP, smem_u32(smem + kBig), b0 + s * 2 * kSmall + kSmall);
             commit_elect(c.s_full);
+            if (j < first) commit_elect(&c.b_empty[s]);
             return true;
         };
         ok = ok && scores(0);
-        for (int j = 0; j < kb.n && ok; ++j) {
-            if (j + 1 < kb.n) ok = scores(j + 1);
-            ok = ok && warp_wait(&c.ready[j & 1], (j >> 1) & 1, c.abort_flag);
+        for (int j = 0; j < steps && ok; ++j) {
+            if (j + 1 < steps) ok = scores(j + 1);
+            if (j < first) continue;
+            ok = ok && warp_wait(&c.ready[j & 1], ((j >> 1) - ((first + 1 - (j & 1)) >> 1)) & 1, c.abort_flag);
             if (!ok) break;
             tc_fence_after();
-            mma_tn<T>(tmQ, tmS + (j & 1) * 64, b0 + (j % kStages) * 2 * kSmall, j > 0);
+            mma_tn<T>(tmQ, tmS + (j & 1) * 64, b0 + (j % kStages) * 2 * kSmall, j > first);
             commit_elect(&c.b_empty[j % kStages]);
-            if (j == kb.n - 1) commit_elect(c.done);
+            if (j == steps - 1) commit_elect(c.done);
         }
         if (!ok) drain_mmas(c);
     } else {
         // ------------------------------------------------------------ math
-        // delta: two threads a row, 32 products each
+        // delta: two threads a row, half of the sum each
         float part = 0.0f, nlse = 0.0f;
         const size_t at = ((size_t)t.batch * a.Hq + head) * a.L + t.start + tok;
-        if (live) {
+        if (live) nlse = -a.lse[at] * kLog2e;
+        if (live && first == 0) {
             const size_t off = (((size_t)t.batch * a.L + t.start + tok) * a.Hq + head) * kD + half * 32;
             const uint4* po = reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + off);
             const uint4* pd = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + off);
-            nlse = -a.lse[at] * kLog2e;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const uint4 x = po[u], y = pd[u];
@@ -280,20 +295,41 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
                 }
             }
         }
-        row_s[half * 128 + r] = part;
-        named_bar_sync(1, kMathWarps * 32);
-        const float ndelta = -(row_s[r] + row_s[128 + r]);
-        if (live && half == 0) a.delta[at] = -ndelta;
-
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const float sc = a.scale * kLog2e;
-        const float2 sc2 = make_float2(sc, sc), nl2 = make_float2(nlse, nlse), nd2 = make_float2(ndelta, ndelta);
+        const float2 sc2 = make_float2(sc, sc), nl2 = make_float2(nlse, nlse);
         // blocks that every row of this warp sees whole begin in [full_lo, full_hi]
         const bool warp_live = __all_sync(0xffffffffu, live);
         const int full_lo = i1 - a.w, full_hi = imin(i0 + 1, t.n) - 64;
         bool ok = true;
-        for (int j = 0; j < kb.n; ++j) {
-            const int c0 = key_block(kb, j) * 64;
+        for (int j = 0; j < first; ++j) {
+            const int c0 = key0(j) + 32 * half;
+            ok = warp_wait(c.s_full, j & 1, c.abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            float x[32], y[32];
+            tmem_ld32f(tmS + lane_off + (j & 1) * 64 + half * 32, x);
+            tmem_ld32f(tmP + lane_off + half * 32, y);
+            tmem_ld_wait();
+            regs_ready<32>(x);
+            regs_ready<32>(y);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.free_);
+            const uint32_t bits = live ? visible_bits32(tok, c0, t.n, a.w, a.sinks) : 0u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if ((bits >> e) & 1) part = fmaf(ex2(fmaf(x[e], sc, nlse)), y[e], part);
+        }
+        row_s[half * 128 + r] = part;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.halves);
+        ok = ok && warp_wait(c.halves, 0, c.abort_flag);
+        const float ndelta = ok ? -(row_s[r] + row_s[128 + r]) : 0.0f;
+        if (live && half == 0) a.delta[at] = -ndelta;
+        const float2 nd2 = make_float2(ndelta, ndelta);
+        for (int j = first; j < steps && ok; ++j) {
+            const int c0 = key0(j);
             const uint32_t tS = tmS + lane_off + (j & 1) * 64 + half * 32;
             const bool full = warp_live && c0 <= full_hi && c0 >= full_lo;
             ok = warp_wait(c.s_full, j & 1, c.abort_flag);

@@ -367,3 +367,26 @@ def test_a_captured_pass_of_many_items_repeats_bit_for_bit():
         torch.cuda.synchronize()
         assert torch.equal(o, out) and torch.equal(l, lse)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,w", [([1] * 50, 9), ([200, 1, 65], 0)])
+def test_rows_that_see_one_key_have_no_gradient_of_scores(dtype, lens, w):
+    """P = 1, so dS = P (dP - delta) = 0: what is left is dP (1 - P) twice
+    over, with |1 - P| off by the fp32 scores (64 products of |q k| scale, 10
+    at most here, each rounding 2^-24 of that) and the approximate
+    exponential and logarithm (2^-22): below 2^-13."""
+    Hq, Hkv, T = 4, 2, sum(lens)
+    q, k, v = (_rand((T, H, 64), dtype, 50 + H + i) for i, H in enumerate((Hq, Hkv, Hkv)))
+    do = _rand((T, Hq * 64), dtype, 60)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    out, lse = lf.lf_window_attention_forward(q, k, v, w, 0, cu_seqlens=cu)
+    dq, dk, dv = lf.lf_window_attention_backward(q, k, v, out, lse, do, w, 0, cu_seqlens=cu)
+    G = Hq // Hkv
+    kk, vv = (t.double().repeat_interleave(G, 1) for t in (k, v))
+    dp = (do.double().view(T, Hq, 64).abs() * vv.abs()).sum(-1, keepdim=True)
+    assert float((q.double() * kk).abs().sum(-1).max()) * 0.125 < 10
+    off = 2.0 ** -13 * 0.125 * dp
+    assert bool((dq.double().abs() <= off * kk.abs() + 2.0 ** -24).all())
+    assert bool((dk.double().abs() <= (off * q.double().abs()).view(T, Hkv, G, 64).sum(2) + 2.0 ** -24).all())
+    assert torch.equal(dv, do.float().view(T, Hkv, G, 64).sum(2).to(dv.dtype))  # P rounds to 1
