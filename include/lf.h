@@ -459,7 +459,7 @@ typedef struct {
  * both cu_seqlens and seq_lens), LF_ERR_DTYPE, LF_ERR_MISALIGNED (also a
  * stride that is not a multiple of 16 bytes), LF_ERR_TOO_LARGE
  * (n_seqs * Hq * L or n_seqs * sinks >= 2^31, L >= 2^30, n_seqs >= 2^23,
- * Hkv > 65535).
+ * Hkv > 65535, or 2^30 tiles of work and more).
  * Offsets or lengths outside [0, L] or descending are clamped and recorded
  * as LF_ERR_BAD_LENGTHS.  L = 0 is allowed and does nothing.  Asynchronous;
  * no scratch, so calls on different streams may overlap.
@@ -475,7 +475,8 @@ size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int 
 /*
  * lf_window_attention_backward -- gradients of lf_window_attention_forward.
  * With P the softmax (recomputed from lse), dP_ij = dout_i.v_j and
- * delta_i = dout_i.out_i:
+ * delta_i = dout_i.out_i (LF_F16, LF_BF16, rows that may see few keys: its
+ * equal sum_j P_ij dP_ij, free of out's rounding):
  *     dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dP_ij - delta_i),
  *     dq_i = s sum_j dS_ij k_j,   dk_j = s sum_i dS_ij q_i,
  * summed over the Hq / Hkv query heads of a key/value head.  P and dS are

@@ -785,16 +785,17 @@ lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
         !make_heads_map(&mk.dout, dout, a.Hq, a.L, B, G, 64 / G) ||
         !make_heads_map(&mk.k, a.k, a.Hkv, a.L, B, 1, 128) || !make_heads_map(&mk.v, a.v, a.Hkv, a.L, B, 1, 128))
         return LF_ERR_CUDA;
+    const int slots = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.chunk) : 0;
+    const long long sink_items = (long long)slots * ((a.sinks + 127) / 128);
+    const int per_head = token_slots(a.packed(), a.n_seqs, a.L, 128);
+    if (sink_items + per_head > INT32_MAX / 2 / a.Hkv) return LF_ERR_TOO_LARGE;
+    const long long items = (sink_items + per_head) * a.Hkv;
     st = launch_pdl(dq_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, 128 / G), a.Hkv), dim3(kThreads),
                     kSmemBytes, stream, mq, a);
     if (st != LF_OK) return st;
-    const int slots = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.chunk) : 0;
-    const int sink_items = slots * ((a.sinks + 127) / 128), per_head = token_slots(a.packed(), a.n_seqs, a.L, 128);
-    const long long items = ((long long)sink_items + per_head) * a.Hkv;
-    if (items > INT32_MAX / 2) return LF_ERR_TOO_LARGE;
     const bool many = items >= kRounds * kResident && (128LL + a.w) * G <= kShort * 64;
     st = launch_pdl(many ? dkv_kernel<T, true> : dkv_kernel<T, false>, dim3((unsigned)(many ? kResident : items)),
-                    dim3(kThreads), kSmemBytes, stream, mk, a, slots, sink_items, per_head, (int)items);
+                    dim3(kThreads), kSmemBytes, stream, mk, a, slots, (int)sink_items, per_head, (int)items);
     if (st == LF_OK && a.sinks > 0) st = launch_sink_reduce(a, stream);
     return st;
 }
