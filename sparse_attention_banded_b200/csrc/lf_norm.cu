@@ -15,6 +15,10 @@
 // on this one.  The backward kernel keeps each thread's share of dgamma and
 // dbeta in registers over all rows of its block; a second kernel adds the
 // blocks' sums.  All sums have a fixed order (no atomics).
+// Measured, forward and backward: 16384 x 1024 bf16 44 us, 3.8 of the 6.6
+// TB/s of a copy (168 MB; the second kernel's sums, 5 us, and two rows in
+// flight per group in the backward, which registers bound, keep it there);
+// 5001 x 1537 fp32, an odd width by single elements, 37 us, 4.1 TB/s.
 #include "lf_convert.cuh"
 #include "lf_tc_tiles.cuh"
 #include "lf_window.h"

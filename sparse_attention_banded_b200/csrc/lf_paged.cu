@@ -2,7 +2,8 @@
 //
 // Token t of sequence b's n_b new ones goes to position kv_lens[b] - n_b + t.
 // A copy, bound by HBM (and by its launch for a few tokens): 8 threads move
-// one 128-byte row of k and of v with 16-byte accesses.
+// one 128-byte row of k and of v with 16-byte accesses.  4.6 us for 2048
+// tokens of 4 heads, as for one.
 #include "lf_tc_tiles.cuh"
 
 namespace lf {

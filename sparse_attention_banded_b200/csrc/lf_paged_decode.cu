@@ -12,6 +12,10 @@
 // interleaved by byte permutes.  (These are memory-bound 16-row products;
 // tcgen05 tiles have 128 rows.)
 //
+// 48 tokens over contexts to 8192, 16 / 4 heads, bf16: 44 us, 4.4 TB/s of the
+// 6.6 of a copy, and 54 us with the keys through shared memory by TMA (a CTA
+// then holds fewer bytes in flight than its registers do).
+//
 // Each warp runs an online softmax over its keys; the warps' results are
 // joined in shared memory, the chunks' by the merge kernel: with the log2-
 // sum-exp e_s and normalised row o_s of chunk s,

@@ -11,7 +11,10 @@
 //             log-sum-exp.  Each sum has one owner and one order: no atomics.
 //
 // The three products of a block pair run from shared memory with a 4 x 4
-// register tile per thread (8 float4 loads for 64 FMAs).
+// register tile per thread (8 float4 loads for 64 FMAs).  Shared-memory
+// bandwidth bounds them when the tiles fill the GPU; 512 tokens, 2 heads,
+// window 64 (a forward and backward of 110 us) are 16 tiles a kernel, each a
+// chain of a few blocks.
 #include "lf_convert.cuh"
 #include "lf_window.h"
 
