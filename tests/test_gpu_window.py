@@ -390,3 +390,11 @@ def test_rows_that_see_one_key_have_no_gradient_of_scores(dtype, lens, w):
     assert bool((dq.double().abs() <= off * kk.abs() + 2.0 ** -24).all())
     assert bool((dk.double().abs() <= (off * q.double().abs()).view(T, Hkv, G, 64).sum(2) + 2.0 ** -24).all())
     assert torch.equal(dv, do.float().view(T, Hkv, G, 64).sum(2).to(dv.dtype))  # P rounds to 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("n", [1, 3, 400])
+def test_only_empty_sequences(dtype, n):
+    """Rows of no sequence, or padding throughout."""
+    _packed([0] * n, 3, 3, 10, 2, dtype, tail=5)
+    _padded(dtype, [0] * n, 4, 3, 3, 1, 1, "bhld")
