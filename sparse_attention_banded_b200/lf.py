@@ -444,6 +444,12 @@ def _new(t, like, dtype, shape, name):
     return _want(name, t, dtype, shape)
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and dtype (0.5 us less than
+    new_empty, of a call's 15)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _workspace(t, like, need):
     """(tensor, address, bytes) of the caller's workspace or a new one."""
     if t is None:
@@ -543,7 +549,9 @@ def lf_window_attention_backward(q, k, v, out, lse, dout, w: int, sinks: int = 0
     _want("dout", dout, dtype, o_shape)
     _want("lse", lse, torch.float32, l_shape)
     with _on(q, stream, k, v, out, lse, dout, cu_seqlens, seq_lens, dq, dk, dv, workspace):
-        dq, dk, dv = (t.new_empty(t.shape) if g is None else g for g, t in ((dq, q), (dk, k), (dv, v)))
+        dq = _like(q) if dq is None else dq
+        dk = _like(k) if dk is None else dk
+        dv = _like(v) if dv is None else dv
         need = 0
         if workspace is None:
             need = max(256, lib().lf_window_attention_backward_workspace_bytes(
@@ -646,7 +654,7 @@ def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None,
             _want("gamma", gamma, torch.float32, (N,))
         if beta is not None:
             _want("beta", beta, torch.float32, (N,))
-        out = _new(out, x, x.dtype, x.shape, "out")
+        out = _like(x) if out is None else _want("out", out, x.dtype, x.shape)
         if mean is None and rstd is None:
             mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind(0)
         else:
@@ -675,7 +683,7 @@ def lf_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta
             _want("gamma", gamma, torch.float32, (N,))
         _want("mean", mean, torch.float32, (rows,))
         _want("rstd", rstd, torch.float32, (rows,))
-        dx = _new(dx, x, x.dtype, x.shape, "dx")
+        dx = _like(x) if dx is None else _want("dx", dx, x.dtype, x.shape)
         if param_grads or dgamma is not None:
             dgamma = _new(dgamma, x, torch.float32, (N,), "dgamma")
         if param_grads or dbeta is not None:
