@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 import re
 
@@ -460,13 +461,16 @@ def _workspace(t, like, need):
     return t, _dense(t), t.numel() * t.element_size()
 
 
-_INT32 = range(-(1 << 31), 1 << 31)
-
-
 def _int32(**values):
+    """The values as Python ints; any type that stands for a whole number will
+    do (NumPy's, a one-element integer tensor)."""
+    ints = []
     for name, x in values.items():
-        if x not in _INT32:
+        x = operator.index(x)
+        if not -(1 << 31) <= x < 1 << 31:
             raise ValueError("%s: %d is not an int32" % (name, x))
+        ints.append(x)
+    return ints
 
 
 def _heads(name, t, shape=None, dtype=None):
@@ -518,7 +522,7 @@ def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 
     row when padded; or packed q [T, Hq, 64], k, v [T, Hkv, 64] with
     cu_seqlens [n + 1] int32.  Returns (out [B, L, Hq*64] or [T, Hq*64], lse
     [B, Hq, L] or [1, Hq, T] float32, for the backward pass)."""
-    _int32(w=w, sinks=sinks)
+    w, sinks = _int32(w=w, sinks=sinks)
     n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
     with _on(q, stream, k, v, cu_seqlens, seq_lens, out, lse):
         out = _new(out, q, q.dtype, o_shape, "out")
@@ -542,7 +546,7 @@ def lf_window_attention_backward(q, k, v, out, lse, dout, w: int, sinks: int = 0
     returned them, dout like out (contiguous).  dq, dk, dv may be strided
     views (of one gradient of a fused projection, say); without them they are
     allocated like q, k, v, contiguous.  Returns (dq, dk, dv)."""
-    _int32(w=w, sinks=sinks)
+    w, sinks = _int32(w=w, sinks=sinks)
     n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
     dtype = q.dtype
     _want("out", out, dtype, o_shape)
@@ -613,7 +617,7 @@ def lf_paged_attention_forward(q, k_cache, v_cache, block_table, cu_seqlens, kv_
     cache, which holds their own keys and values already
     (:func:`lf_paged_cache_append`).  Returns out [T, Hq*64]."""
     n, T, Hkv, max_pages, num_pages, page_size = _paged_shape(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens)
-    _int32(w=w, sinks=sinks, max_q_len=max_q_len)
+    w, sinks, max_q_len = _int32(w=w, sinks=sinks, max_q_len=max_q_len)
     Hq = q.shape[1]
     with _on(q, stream, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, workspace):
         out = _new(out, q, q.dtype, (T, Hq * 64), "out")
