@@ -473,6 +473,13 @@ def _int32(**values):
     return ints
 
 
+def _fits(name, *sizes):
+    """Refuses sizes that the C interface's int would cut off."""
+    for n in sizes:
+        if n >> 31:
+            raise ValueError("%s: size %d is not an int32" % (name, n))
+
+
 def _heads(name, t, shape=None, dtype=None):
     """lf_heads of [B, H, T, 64], or of packed [T, H, 64]."""
     if dtype is not None:
@@ -494,6 +501,7 @@ def _window_shape(q, k, v, cu_seqlens, seq_lens):
     kv = k.shape
     if k.dtype is not dtype or v.dtype is not dtype or v.shape != kv or len(kv) != len(shape):
         raise ValueError("k, v: expected two [.., Hkv, .., 64] of %s like q, got %s and %s" % (dtype, tuple(kv), tuple(v.shape)))
+    _fits("q, k", *shape, kv[1])
     if packed:
         L, Hq, _ = shape
         Hkv = kv[1]
@@ -536,7 +544,8 @@ def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 
 
 def lf_window_attention_backward_workspace_bytes(packed: bool, n_seqs: int, Hq: int, Hkv: int, L: int, w: int,
                                                  sinks: int) -> int:
-    return lib().lf_window_attention_backward_workspace_bytes(int(packed), n_seqs, Hq, Hkv, L, w, sinks)
+    return lib().lf_window_attention_backward_workspace_bytes(
+        int(packed), *_int32(n_seqs=n_seqs, Hq=Hq, Hkv=Hkv, L=L, w=w, sinks=sinks))
 
 
 def lf_window_attention_backward(q, k, v, out, lse, dout, w: int, sinks: int = 0, scale: float = 0.125,
@@ -583,6 +592,9 @@ def _paged_shape(new, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
     if block_table.dim() != 2 or block_table.dtype is not i32:
         raise ValueError("block_table: expected [n_seqs, max_pages] int32")
     n, max_pages = block_table.shape
+    _fits("block_table", n, max_pages)
+    _fits("k_cache", *cache)
+    _fits("new tokens", new.shape[0], new.shape[1])
     _want("cu_seqlens", cu_seqlens, i32, (n + 1,))
     _want("kv_lens", kv_lens, i32, (n,))
     return n, new.shape[0], cache[1], max_pages, cache[0], cache[2]
@@ -606,7 +618,9 @@ def lf_paged_cache_append(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_le
 
 def lf_paged_attention_workspace_bytes(n_seqs: int, Hq: int, Hkv: int, T: int, max_q_len: int, max_pages: int,
                                        page_size: int, w: int, sinks: int) -> int:
-    return lib().lf_paged_attention_workspace_bytes(n_seqs, Hq, Hkv, T, max_q_len, max_pages, page_size, w, sinks)
+    return lib().lf_paged_attention_workspace_bytes(
+        *_int32(n_seqs=n_seqs, Hq=Hq, Hkv=Hkv, T=T, max_q_len=max_q_len, max_pages=max_pages, page_size=page_size, w=w,
+                sinks=sinks))
 
 
 def lf_paged_attention_forward(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len: int,
@@ -641,6 +655,7 @@ def _rows(name, t):
         raise ValueError("%s: expected [..., N]" % name)
     N = shape[-1]
     rows = t.numel() // N if N else 0
+    _fits(name, rows, N)
     if t.is_contiguous():
         return t.data_ptr(), rows, N, N
     if len(shape) == 2 and (t.stride(1) == 1 or N == 1):
@@ -652,8 +667,8 @@ def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None,
     """Layer norm of the rows of x [..., N]; gamma, beta [N] float32 or None.
     Returns (y, mean, rstd), mean and rstd [rows] float32 for the backward
     pass."""
+    px, rows, N, stride = _rows("x", x)
     with _on(x, stream, gamma, beta, out, mean, rstd):
-        px, rows, N, stride = _rows("x", x)
         if gamma is not None:
             _want("gamma", gamma, torch.float32, (N,))
         if beta is not None:
@@ -672,7 +687,7 @@ def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None,
 
 
 def lf_layer_norm_backward_workspace_bytes(rows: int, N: int) -> int:
-    return lib().lf_layer_norm_backward_workspace_bytes(rows, N)
+    return lib().lf_layer_norm_backward_workspace_bytes(*_int32(rows=rows, N=N))
 
 
 def lf_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, param_grads: bool = True,
@@ -680,8 +695,8 @@ def lf_layer_norm_backward(dy, x, gamma, mean, rstd, dx=None, dgamma=None, dbeta
     """Gradients of :func:`lf_layer_norm_forward` (mean, rstd as it returned
     them).  Returns (dx, dgamma, dbeta); with param_grads False only those of
     dgamma, dbeta that were passed in are written."""
+    px, rows, N, xs = _rows("x", x)
     with _on(x, stream, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace):
-        px, rows, N, xs = _rows("x", x)
         pdy, _, _, dys = _rows("dy", _want("dy", dy, x.dtype, x.shape))
         if gamma is not None:
             _want("gamma", gamma, torch.float32, (N,))

@@ -48,3 +48,43 @@ def test_other_numbers_are_refused_at_once(w, error):
     with pytest.raises(error):
         lf.lf_window_attention_forward(q, k, k, 4, sinks=w)
     assert time.monotonic() - t0 < 5
+
+
+def _wide(*shape, dtype=torch.float16):
+    """A tensor of any shape over one element."""
+    return torch.zeros((), dtype=dtype).expand(shape)
+
+
+BIG = (1 << 32) + 8  # cut to 32 bits this would be 8
+
+
+def test_sizes_past_32_bits_are_refused():
+    """A size that the C interface's int cannot hold is an error, not another
+    size."""
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="int32"):
+        lf.lf_window_attention_forward(_wide(BIG, 1, 64), _wide(BIG, 1, 64), _wide(BIG, 1, 64), 4,
+                                       cu_seqlens=torch.zeros(2, dtype=i32))
+    q = _wide(1, 1, BIG, 64)
+    with pytest.raises(ValueError, match="int32"):
+        lf.lf_window_attention_forward(q, q, q, 4)
+    with pytest.raises(ValueError, match="int32"):
+        lf.lf_window_attention_backward(q, q, q, _wide(1, BIG, 64), _wide(1, 1, BIG, dtype=torch.float32),
+                                        _wide(1, BIG, 64), 4)
+    q, cache, cu, kv = _wide(1, 1, 64), _wide(4, 1, 16, 64), torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32)
+    for c, table in ((cache, _wide(1, BIG, dtype=i32)), (_wide(BIG, 1, 16, 64), _wide(1, 4, dtype=i32)),
+                     (_wide(4, 1, BIG, 64), _wide(1, 4, dtype=i32))):
+        with pytest.raises(ValueError, match="int32"):
+            lf.lf_paged_attention_forward(q, c, c, table, cu, kv, 1)
+        with pytest.raises(ValueError, match="int32"):
+            lf.lf_paged_cache_append(q, q, c, c, table, cu, kv)
+    for x in (_wide(BIG, 1), _wide(1, BIG)):
+        with pytest.raises(ValueError, match="int32"):
+            lf.lf_layer_norm_forward(x)
+        with pytest.raises(ValueError, match="int32"):
+            lf.lf_layer_norm_backward(x, x, None, torch.zeros(8), torch.zeros(8))
+    for call in (lambda: lf.lf_layer_norm_backward_workspace_bytes(BIG, 64),
+                 lambda: lf.lf_window_attention_backward_workspace_bytes(False, 1, 1, 1, BIG, 4, 0),
+                 lambda: lf.lf_paged_attention_workspace_bytes(1, 1, 1, 1, 1, BIG, 16, 4, 0)):
+        with pytest.raises(ValueError, match="int32"):
+            call()
