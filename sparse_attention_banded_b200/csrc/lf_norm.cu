@@ -338,13 +338,13 @@ int threads_per_row(int N) {
 constexpr int kMaxBlocks = 2 * 148;
 int backward_blocks(int rows, int N) {
     const int tpr = threads_per_row(N), per = tpr > 256 ? 1 : 256 / tpr;
-    return imin((rows + per - 1) / per, kMaxBlocks);
+    return imin((rows - 1) / per + 1, kMaxBlocks);  // (rows > 0, up to 2^31 - 1)
 }
 
 template <typename T, int TPR, int EPT, int VEC>
 lf_status run_forward(const NormArgs& a, cudaStream_t stream) {
     constexpr int kRows = block_threads<TPR>() / TPR;
-    const int blocks = imin((a.rows + kRows - 1) / kRows, 2 * 148);
+    const int blocks = imin((a.rows - 1) / kRows + 1, 2 * 148);
     return launch_pdl(forward_kernel<T, TPR, EPT, VEC>, dim3(blocks), dim3(block_threads<TPR>()), 0, stream, a);
 }
 

@@ -11,10 +11,10 @@ import torch
 from sparse_attention_banded_b200 import build, lf
 
 
-@pytest.fixture(scope="module")
-def L():
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
     build.build()
-    return lf.lib()
+    lf.lib()
 
 
 class Window(enum.IntEnum):
@@ -88,3 +88,14 @@ def test_sizes_past_32_bits_are_refused():
                  lambda: lf.lf_paged_attention_workspace_bytes(1, 1, 1, 1, 1, BIG, 16, 4, 0)):
         with pytest.raises(ValueError, match="int32"):
             call()
+
+
+def test_layer_norm_workspace_to_the_last_row_count():
+    """At most 296 blocks (two per SM) of 2 N sums, for any number of rows."""
+    top = (1 << 31) - 1
+    for N in (1, 64, 513, 4096, 16384):
+        full = 296 * 2 * N * 4
+        for rows in (1 << 20, top - 300, *range(top - 9, top + 1)):
+            assert lf.lf_layer_norm_backward_workspace_bytes(rows, N) == full, (rows, N)
+    assert lf.lf_layer_norm_backward_workspace_bytes(1, 64) == 2 * 64 * 4
+    assert lf.lf_layer_norm_backward_workspace_bytes(9, 64) == 2 * 2 * 64 * 4  # eight rows a block
