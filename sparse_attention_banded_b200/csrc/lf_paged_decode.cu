@@ -242,16 +242,17 @@ decode_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Paged
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int d = 0; d < 8; ++d) x[d] *= inv;
-        const size_t row = (size_t)(start + r / G) * a.Hq + hk * G + r % G;
+        const int head = hk * G + r % G;
         if (whole) {
+            const size_t row = (size_t)(start + r / G) * a.Hq + head;
             reinterpret_cast<uint4*>(out + row * kD)[e & 7] = make_uint4(
                 Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]), Pair<T>::pack(x[4], x[5]), Pair<T>::pack(x[6], x[7]));
         } else {
-            const size_t at = (size_t)piece * ((size_t)a.T * a.Hq) + row;
-            float4* d = reinterpret_cast<float4*>(pl.o + at * kD + c);
+            const size_t at = ((size_t)piece * pl.decode_tokens + pl.decode_slot(b, start, r / G)) * a.Hq + head;
+            float4* d = reinterpret_cast<float4*>(pl.decode_o + at * kD + c);
             d[0] = make_float4(x[0], x[1], x[2], x[3]);
             d[1] = make_float4(x[4], x[5], x[6], x[7]);
-            if (c == 0) pl.lse[at] = sum == 0.f ? -INFINITY : top + log2f(sum);
+            if (c == 0) pl.decode_lse[at] = sum == 0.f ? -INFINITY : top + log2f(sum);
         }
     }
 }
@@ -305,15 +306,26 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     if (tok < start || tok >= start + n) return;
     int kv, first;
     if (!paged_seq(a, b, n, kv, first, false)) return;
+    // the pieces: how many, how many rows apart, where this token's are
     int pieces;
+    const float *po, *pe;
+    size_t step, at0;
     if (pl.decode && n * G <= kRows) {
         pieces = (decode_tiles(first, n, kv, a.w, a.sinks).n + pl.chunk - 1) / pl.chunk;
+        po = pl.decode_o;
+        pe = pl.decode_lse;
+        step = (size_t)pl.decode_tokens * a.Hq;
+        at0 = (size_t)pl.decode_slot(b, start, tok - start) * a.Hq + h0;
     } else {
         const int TQ = 128 / G, t0 = (tok - start) / TQ * TQ;
         pieces = (tile_key_blocks(first, t0, imin(t0 + TQ, n), kv, a.w, a.sinks).n + pl.per - 1) / pl.per;
+        po = pl.o;
+        pe = pl.lse;
+        step = (size_t)a.T * a.Hq;
+        at0 = (size_t)tok * a.Hq + h0;
     }
     if (pieces <= 1) return;  // written whole
-    const size_t step = (size_t)a.T * a.Hq, row0 = (size_t)tok * a.Hq + h0;
+    const size_t row0 = (size_t)tok * a.Hq + h0;
     auto store = [&](const Joined& j, size_t row) {
         const float inv = j.sum == 0.f ? 0.f : 1.f / j.sum;
         reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * kD)[lane] =
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     if constexpr (kBlock) {
         static_assert(kEach == 1, "one row per block");
         const int part = threadIdx.x >> 4;
-        parts[part][lane] = join(pl.o + row0 * kD + 4 * lane, pl.lse + row0, step, pieces, part, 16);
+        parts[part][lane] = join(po + at0 * kD + 4 * lane, pe + at0, step, pieces, part, 16);
         __syncthreads();
         if (part > 0) return;
         Joined j = parts[0][lane];
@@ -331,7 +343,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     } else {
 #pragma unroll
         for (int h = half; h < kEach; h += 2)
-            if (h0 + h < a.Hq) store(join(pl.o + (row0 + h) * kD + 4 * lane, pl.lse + row0 + h, step, pieces, 0, 1), row0 + h);
+            if (h0 + h < a.Hq) store(join(po + (at0 + h) * kD + 4 * lane, pe + at0 + h, step, pieces, 0, 1), row0 + h);
     }
 }
 

@@ -4,6 +4,8 @@
 // both kernels and the merge agree on.
 #pragma once
 
+#include <stddef.h>
+
 #include "lf_visible.h"
 
 namespace lf {
@@ -19,9 +21,22 @@ struct PagedPlan {
     int per;              // tensor cores: blocks of 64 keys per CTA
     int tensor_splits;    // pieces of a tile, at most
     bool ahead;           // few items: two CTAs per SM, worked on ahead
-    float* o;             // [splits][T * Hq][64]
-    float* lse;           // [splits][T * Hq], log2
+    // Partial rows of contexts in several pieces: normalised sums and their
+    // log2-sum-exp.  The decode kernel cuts a context into far more pieces
+    // than the tensor cores do, of far fewer rows, so each has its own.
+    int decode_tokens;    // tokens that the decode kernel may work on
+    int decode_each;      // of one sequence; 0: counted over the batch's tokens
+    float *decode_o, *decode_lse;  // [decode_splits][decode_tokens * Hq][64], [..]
+    float *o, *lse;                // [tensor_splits][T * Hq][64], [..]
     LF_HD int splits() const { return imax(decode ? decode_splits : 1, tensor ? tensor_splits : 1); }
+    // Where the decode kernel leaves the token t of sequence b, which starts at `start`.
+    LF_HD int decode_slot(int b, int start, int t) const { return decode_each ? b * decode_each + t : start + t; }
+    size_t decode_rows(int Hq) const {
+        return decode && decode_splits > 1 ? (size_t)decode_splits * decode_tokens * Hq : 0;
+    }
+    size_t tensor_rows(int T, int Hq) const {
+        return tensor && tensor_splits > 1 ? (size_t)tensor_splits * T * Hq : 0;
+    }
 };
 
 // The tiles of 8 keys a sequence's n new tokens from position `first` see.
@@ -57,6 +72,10 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
     // (with n_seqs * max_q tokens every sequence has max_q)
     p.decode = G <= kDecodeRows && !(p.tensor && (long long)n_seqs * max_q == T);
     if (p.decode) {
+        // at most kDecodeRows / G tokens of each sequence, and T in all
+        const int each = kDecodeRows / G;
+        p.decode_each = (long long)n_seqs * each < T ? each : 0;
+        p.decode_tokens = p.decode_each ? n_seqs * each : T;
         // About two rounds of CTAs (three of 4 warps fit an SM) over the
         // widest contexts, 128 to 1024 keys each: fewer, and a warp has no
         // second step to load under its first; more, and ragged contexts

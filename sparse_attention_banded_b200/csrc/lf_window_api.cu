@@ -214,9 +214,8 @@ size_t lf_paged_attention_workspace_bytes(int n_seqs, int Hq, int Hkv, int T, in
     const int width = max_pages * page_size;
     const PagedPlan p =
         paged_plan(n_seqs, Hq, Hkv, T, imin(max_q_len, T), width, imin(w, width), imin(sinks, width));
-    if (p.splits() <= 1) return 0;
-    const size_t rows = (size_t)p.splits() * T * Hq;
-    return align256(rows * 64 * sizeof(float)) + align256(rows * sizeof(float));
+    const size_t rows = p.decode_rows(Hq) + p.tensor_rows(T, Hq);
+    return rows * 64 * sizeof(float) + align256(rows * sizeof(float));
 }
 
 lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache, const lf_heads* v_cache,
@@ -262,8 +261,11 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
     a.status = d->status;
     PagedPlan plan = paged_plan(n_seqs, Hq, Hkv, T, a.max_q, max_pages * page_size, a.w, a.sinks);
     if (plan.decode && (long long)n_seqs * plan.decode_splits >= kInt31) return LF_ERR_TOO_LARGE;
-    plan.o = static_cast<float*>(workspace);
-    plan.lse = plan.o + align256((size_t)plan.splits() * T * Hq * 64 * sizeof(float)) / sizeof(float);
+    const size_t decode_rows = plan.decode_rows(Hq), rows = decode_rows + plan.tensor_rows(T, Hq);
+    plan.decode_o = static_cast<float*>(workspace);
+    plan.o = plan.decode_o + decode_rows * 64;
+    plan.decode_lse = plan.decode_o + rows * 64;
+    plan.lse = plan.decode_lse + decode_rows;
     return launch_paged_forward(a, plan, (cudaStream_t)stream);
 }
 

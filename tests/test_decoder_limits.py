@@ -1,7 +1,9 @@
 """Limits of the decoder operators that need no GPU: how whole numbers reach
 the library, sizes at the ends of their ranges, and the memory that a call
 asks for."""
+import ctypes
 import enum
+import subprocess
 import time
 
 import numpy as np
@@ -15,6 +17,33 @@ from sparse_attention_banded_b200 import build, lf
 def _lib():
     build.build()
     lf.lib()
+
+
+SRC = r'''
+#include "lf_paged_split.h"
+using namespace lf;
+extern "C" {
+void plan(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int* o) {
+    PagedPlan p = paged_plan(n, Hq, Hkv, T, mq, width, w, s);
+    o[0] = p.decode; o[1] = p.tensor; o[2] = p.chunk; o[3] = p.decode_splits; o[4] = p.per; o[5] = p.tensor_splits;
+}
+void slot(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int b, int start, int t, int* o) {
+    PagedPlan p = paged_plan(n, Hq, Hkv, T, mq, width, w, s);
+    o[0] = p.decode_slot(b, start, t); o[1] = p.decode_tokens;
+}
+}
+'''
+
+
+@pytest.fixture(scope="module")
+def P(tmp_path_factory):
+    """The index arithmetic, compiled for the host."""
+    d = tmp_path_factory.mktemp("limits")
+    (d / "limits.cpp").write_text(SRC)
+    so = str(d / "limits.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", "-I", build.CSRC, str(d / "limits.cpp"), "-o", so], check=True)
+    return ctypes.CDLL(so)
 
 
 class Window(enum.IntEnum):
@@ -99,3 +128,43 @@ def test_layer_norm_workspace_to_the_last_row_count():
             assert lf.lf_layer_norm_backward_workspace_bytes(rows, N) == full, (rows, N)
     assert lf.lf_layer_norm_backward_workspace_bytes(1, 64) == 2 * 64 * 4
     assert lf.lf_layer_norm_backward_workspace_bytes(9, 64) == 2 * 2 * 64 * 4  # eight rows a block
+
+
+@pytest.mark.parametrize("n,T,max_q,Hq,Hkv,w,sinks", [
+    (17, 4096 + 16, 4096, 32, 8, 1 << 30, 0), (16, 8192 + 15, 8192, 32, 8, 1 << 30, 0), (2, 2049, 2048, 32, 8, 1 << 30, 0),
+    (8, 2401, 301, 32, 8, 1 << 30, 0), (300, 2000, 700, 8, 1, 4096, 4), (40, 40, 1, 16, 4, 1 << 30, 0),
+    (3, 900, 300, 5, 1, 1 << 30, 0)])
+def test_a_prompt_chunk_does_not_pay_for_single_tokens_pieces(P, n, T, max_q, Hq, Hkv, w, sinks):
+    """Over a table of 131072 positions: the decode kernel's many pieces are
+    rows of at most 16 / G tokens of a sequence (and T in all), the tensor
+    cores' few pieces rows of all T; 260 bytes a row and head."""
+    width, G = 131072, Hq // Hkv
+    o = (ctypes.c_int * 6)()
+    P.plan(n, Hq, Hkv, T, max_q, width, min(w, width), sinks, o)
+    decode, tensor, _, pieces8, _, pieces64 = o
+    rows = (decode and pieces8 > 1 and pieces8 * min(n * (16 // G), T)) + (tensor and pieces64 > 1 and pieces64 * T)
+    got = lf.lf_paged_attention_workspace_bytes(n, Hq, Hkv, T, max_q, width // 16, 16, w, sinks)
+    assert 260 * Hq * rows <= got < 260 * Hq * rows + 256
+
+
+def test_workspace_of_a_chunk_next_to_single_tokens():
+    """One chunk of 4096 tokens and 16 single ones: the decode rows' 128
+    pieces are 72 MB at most, the chunk's pieces 34 MB each."""
+    assert lf.lf_paged_attention_workspace_bytes(17, 32, 8, 4112, 4096, 8192, 16, 1 << 30, 0) <= 300 << 20
+
+
+@pytest.mark.parametrize("n,T,G", [(5, 100, 1), (5, 100, 4), (5, 12, 4), (5, 20, 4), (1, 16, 1), (7, 9, 16), (3, 50, 5)])
+def test_decode_slots_are_apart_and_inside(P, n, T, G):
+    """Every token of a sequence short enough for the decode kernel has a slot
+    of its own below decode_tokens."""
+    lens = [(3 * b + 1) % (16 // G + 2) for b in range(n)]
+    while sum(lens) > T:
+        lens[lens.index(max(lens))] -= 1
+    o = (ctypes.c_int * 2)()
+    seen, start = set(), 0
+    for b, m in enumerate(lens):
+        for t in range(m if m * G <= 16 else 0):
+            P.slot(n, G, 1, T, max(lens), 4096, 4096, 0, b, start, t, o)
+            assert 0 <= o[0] < o[1] and o[0] not in seen and o[1] == min(T, n * (16 // G))
+            seen.add(o[0])
+        start += m
