@@ -81,8 +81,8 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
         // second step to load under its first; more, and ragged contexts
         // leave SMs idle.
         const long long tiles = most_blocks(max_q, width, w, sinks, 8), all = tiles * n_seqs * Hkv;
-        p.chunk = (int)(all / (2 * 3 * 148));
-        p.chunk = iclamp((p.chunk + 15) / 16 * 16, 16, 128);
+        const long long share = all / (2 * 3 * 148);
+        p.chunk = share > 112 ? 128 : imax(((int)share + 15) / 16 * 16, 16);
         if (tiles > 1024LL * p.chunk) p.chunk = (int)((tiles + 1023) / 1024);  // at most 1024 pieces
         p.decode_splits = (int)((tiles + p.chunk - 1) / p.chunk);
     }

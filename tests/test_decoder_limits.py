@@ -168,3 +168,12 @@ def test_decode_slots_are_apart_and_inside(P, n, T, G):
             assert 0 <= o[0] < o[1] and o[0] not in seen and o[1] == min(T, n * (16 // G))
             seen.add(o[0])
         start += m
+
+
+@pytest.mark.parametrize("n,Hkv", [(1000, 8), (50000, 1000), (116400, 1000), (162600, 1000), (232790, 1000), (2097151, 65535)])
+def test_pieces_of_very_many_contexts(P, n, Hkv):
+    """Many contexts of 131072 positions need no short pieces, however large
+    the count of their tiles grows."""
+    o = (ctypes.c_int * 6)()
+    P.plan(n, Hkv, Hkv, n, 1, 131072, 131072, 0, o)
+    assert o[2] == 128 and o[3] == 128
