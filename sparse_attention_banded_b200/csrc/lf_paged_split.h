@@ -28,6 +28,10 @@ struct PagedPlan {
     int decode_each;      // of one sequence; 0: counted over the batch's tokens
     float *decode_o, *decode_lse;  // [decode_splits][decode_tokens * Hq][64], [..]
     float *o, *lse;                // [tensor_splits][T * Hq][64], [..]
+    // Items of the tensor-core kernel.
+    long long tensor_items(int T, int n_seqs, int Hkv, int G) const {
+        return tensor ? (long long)packed_slots(T, n_seqs, 128 / G) * Hkv * tensor_splits : 0;
+    }
     LF_HD int splits() const { return imax(decode ? decode_splits : 1, tensor ? tensor_splits : 1); }
     // Where the decode kernel leaves the token t of sequence b, which starts at `start`.
     LF_HD int decode_slot(int b, int start, int t) const { return decode_each ? b * decode_each + t : start + t; }

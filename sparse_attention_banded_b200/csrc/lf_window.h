@@ -8,6 +8,10 @@
 
 namespace lf {
 
+// Items of one launch of the persistent kernels: an item's number plus the
+// grid stays in 32 bits.
+constexpr long long kMostItems = INT32_MAX / 2;
+
 // One call, as the kernels see it.  Sequences are packed (cu != NULL: T = L
 // rows in all) or padded (n_seqs x L rows, lens tokens).  w and sinks have
 // been clamped to the longest possible sequence; sinks is 0 when every

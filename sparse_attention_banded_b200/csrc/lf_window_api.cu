@@ -240,6 +240,12 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
         lf_paged_attention_workspace_bytes(n_seqs, Hq, Hkv, T, max_q_len, max_pages, page_size, w, sinks);
     if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need))
         return LF_ERR_WORKSPACE;
+    // (before the first launch: a refused call does nothing)
+    const int width = max_pages * page_size, G = Hq / Hkv;
+    PagedPlan plan =
+        paged_plan(n_seqs, Hq, Hkv, T, imin(max_q_len, T), width, imin(w, width), imin(sinks, width));
+    if (plan.decode && (long long)n_seqs * plan.decode_splits >= kInt31) return LF_ERR_TOO_LARGE;
+    if (plan.tensor_items(T, n_seqs, Hkv, G) > kMostItems) return LF_ERR_TOO_LARGE;
     DeviceCtx* d = current_device(&st);
     if (!d) return st;
     a.cu = cu_seqlens;
@@ -253,14 +259,12 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
     a.max_pages = max_pages;
     a.num_pages = num_pages;
     a.page_shift = log2_of(page_size);
-    a.w = imin(w, max_pages * page_size);
-    a.sinks = imin(sinks, max_pages * page_size);
+    a.w = imin(w, width);
+    a.sinks = imin(sinks, width);
     a.scale = scale;
     a.dtype = dtype;
     a.out = out;
     a.status = d->status;
-    PagedPlan plan = paged_plan(n_seqs, Hq, Hkv, T, a.max_q, max_pages * page_size, a.w, a.sinks);
-    if (plan.decode && (long long)n_seqs * plan.decode_splits >= kInt31) return LF_ERR_TOO_LARGE;
     const size_t decode_rows = plan.decode_rows(Hq), rows = decode_rows + plan.tensor_rows(T, Hq);
     plan.decode_o = static_cast<float*>(workspace);
     plan.o = plan.decode_o + decode_rows * 64;

@@ -788,7 +788,7 @@ lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
     const int slots = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.chunk) : 0;
     const long long sink_items = (long long)slots * ((a.sinks + 127) / 128);
     const int per_head = token_slots(a.packed(), a.n_seqs, a.L, 128);
-    if (sink_items + per_head > INT32_MAX / 2 / a.Hkv) return LF_ERR_TOO_LARGE;
+    if (sink_items + per_head > kMostItems / a.Hkv) return LF_ERR_TOO_LARGE;
     const long long items = (sink_items + per_head) * a.Hkv;
     st = launch_pdl(dq_kernel<T>, dim3(token_slots(a.packed(), a.n_seqs, a.L, 128 / G), a.Hkv), dim3(kThreads),
                     kSmemBytes, stream, mq, a);

@@ -632,7 +632,7 @@ lf_status launch(const Maps& maps, const A& a, const PagedPlan& pp, long long it
     lf_status st;
     DeviceCtx* d = current_device(&st);
     if (!d) return st;
-    if (items > INT32_MAX / 2) return LF_ERR_TOO_LARGE;
+    if (items > kMostItems) return LF_ERR_TOO_LARGE;
     return ahead ? launch_as<T, kPaged, true>(maps, a, pp, (int)items, d, stream)
                  : launch_as<T, kPaged, false>(maps, a, pp, (int)items, d, stream);
 }
@@ -659,7 +659,7 @@ lf_status launch_paged_tc(const PagedArgs& a, const PagedPlan& pp, cudaStream_t 
         !make_heads_map(&maps.k, a.k, a.Hkv, page, a.num_pages, 1, imin(page, kBN)) ||
         !make_heads_map(&maps.v, a.v, a.Hkv, page, a.num_pages, 1, imin(page, kBN)))
         return LF_ERR_CUDA;
-    const long long items = (long long)packed_slots(a.T, a.n_seqs, TQ) * a.Hkv * pp.tensor_splits;
+    const long long items = pp.tensor_items(a.T, a.n_seqs, a.Hkv, G);
     // (items counts slots, of which a batch of single tokens fills few)
     if (a.dtype == LF_F16) return launch<__half, true>(maps, a, pp, items, pp.ahead, stream);
     return launch<__nv_bfloat16, true>(maps, a, pp, items, pp.ahead, stream);

@@ -177,3 +177,14 @@ def test_pieces_of_very_many_contexts(P, n, Hkv):
     o = (ctypes.c_int * 6)()
     P.plan(n, Hkv, Hkv, n, 1, 131072, 131072, 0, o)
     assert o[2] == 128 and o[3] == 128
+
+
+@pytest.mark.parametrize("Hq,max_q", [(17 * 1024, 1), (16 * 1024, 2)])
+def test_too_many_pieces_are_refused_before_anything_runs(Hq, max_q):
+    """2^20 sequences of 1024 key heads are 2^30 items for the tensor cores,
+    next to the decode kernel's (second case) or alone."""
+    heads = lambda: ctypes.byref(lf.Heads(0x10000, 1 << 20, 1 << 14, 64))  # noqa: E731
+    p = ctypes.c_void_p(0x10000)
+    call = lambda n: lf.lib().lf_paged_attention_forward(  # noqa: E731
+        heads(), heads(), heads(), p, p, p, n, Hq, 1024, 1000, max_q, 64, 64, 16, 100, 0, 0.125, 1, p, 1 << 45, None, p)
+    assert call(1 << 20) == 13
