@@ -475,8 +475,9 @@ size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int 
 /*
  * lf_window_attention_backward -- gradients of lf_window_attention_forward.
  * With P the softmax (recomputed from lse), dP_ij = dout_i.v_j and
- * delta_i = dout_i.out_i (LF_F16, LF_BF16, rows that may see few keys: its
- * equal sum_j P_ij dP_ij, free of out's rounding):
+ * delta_i = dout_i.out_i (LF_F16, LF_BF16, where w + 1 + sinks <= 32 and for
+ * a sequence's first 32 rows at least: its equal sum_j P_ij dP_ij, free of
+ * out's rounding):
  *     dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dP_ij - delta_i),
  *     dq_i = s sum_j dS_ij k_j,   dk_j = s sum_i dS_ij q_i,
  * summed over the Hq / Hkv query heads of a key/value head.  P and dS are

@@ -184,12 +184,14 @@ __device__ __forceinline__ uint8_t* smem_base() {
 // ---------------------------------------------------------------- dQ
 // delta comes from out as it was rounded to 16 bits, except where a row may
 // see few keys: there dP and delta nearly cancel, and the rounding would be
-// most of dS (window 1: errors of dQ and dK 2.3 times those of gradients
-// rounded once; a row that sees one key has none of either).  So a tile of
-// few blocks takes them twice, and the first pass sums delta = sum P dP in
-// fp32.  From four blocks on most rows see a hundred keys, and the 16-bit dS
-// is what is left (1.4 times).
-constexpr int kTwice = 3;
+// much of dS.  Such tiles take their blocks twice, and the first pass sums
+// delta = sum P dP in fp32.  They are the tiles of a call whose rows see at
+// most kFewKeys keys, sinks among them, and the first of a sequence (up to
+// kTwice blocks).  Errors of dQ, in those of gradients rounded once, with
+// delta from fp32 and from the rounded out (bf16, emulated): 2 keys 1.4 and
+// 2.2, 3 keys 1.4 and 1.9, 6 keys 1.4 and 1.6, 20 keys 1.41 and 1.48, 132 keys
+// 1.40 and 1.44.  What is left is dS as a 16-bit operand.
+constexpr int kTwice = 3, kFewKeys = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -216,7 +218,8 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
     }
     const int i0 = t.t0, i1 = imin(t.t0 + TQ, t.n) - 1;
     const KeyBlocks kb = key_blocks(i0, i1, t.n, a.w, a.sinks, 64);
-    const int first = kb.n <= kTwice ? kb.n : 0, steps = first + kb.n;  // steps of the first pass, of both
+    const bool few = kb.n <= kTwice || a.w + 1 + a.sinks <= kFewKeys;
+    const int first = few ? kb.n : 0, steps = first + kb.n;  // steps of the first pass, of both
     auto key0 = [&](int j) { return key_block(kb, j < first ? j : j - first) * 64; };
     const Ctx c = setup(smem, warp, lane);
     const uint32_t tmS = c.tmem, tmP = c.tmem + 128, tmQ = c.tmem + 192;

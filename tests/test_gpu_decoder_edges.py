@@ -41,3 +41,54 @@ def test_pieces_of_both_kernels_in_one_call(dtype, q, kv, Hq, Hkv):
     both = lf.lf_paged_attention_workspace_bytes(n, Hq, Hkv, T, max(q), wide, 16, c.w, 0)
     assert 0 < short < both
     c.run().check()
+
+
+def _bound_without_out(q, k, v, w, sinks, do, scale=0.125):
+    """dQ and dK and their bounds where delta is no sum with the rounded out.
+    With e the relative error of a probability (fp32 scores of 64 products,
+    at most S in size, against a log-sum-exp of as many; the exponential and
+    the logarithm 2^-21), u half a step, z the subnormal half step:
+        dP     2^-18 |dout|.|v|                  (64 fp32 products)
+        delta  sum_j p_j (2 e + 2^-18) |dout|.|v_j|
+        dS     E = p (both) + (u + 2 e + 2^-20) |dS| + z
+        dq     scale sum_j E |k_j| + u |dq| + z;  dk likewise."""
+    u, z = half_step(q.dtype), subnormal_half_step(q.dtype)
+    r = reference(q, k, v, 0, w, sinks, scale, do)
+    G = q.shape[0] // k.shape[0]
+    q, k, v, do = q.double(), k.double().repeat_interleave(G, 0), v.double().repeat_interleave(G, 0), do.double()
+    n = q.shape[1]
+    i, j = torch.arange(n, device="cuda")[:, None], torch.arange(n, device="cuda")[None]
+    ok = (j <= i) & ((i - j <= w) | (j < sinks))
+    p = torch.softmax((q @ k.mT * scale).masked_fill(~ok, float("-inf")), -1)
+    S = float((q.abs() @ k.abs().mT * scale).where(ok, 0.0).max())
+    e = 2.0 ** -24 * (128 * S + n + 64) + 2.0 ** -21
+    dp, dpa = do @ v.mT, do.abs() @ v.abs().mT
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    E = p * (2.0 ** -18 * dpa + (2 * e + 2.0 ** -18) * (p * dpa).sum(-1, keepdim=True)) + (u + 2 * e + 2.0 ** -20) * ds.abs()
+    E = E + z * ok
+    b_dq = scale * E @ k.abs() + u * r["dq"].abs() + z
+    b_dk = (scale * E.mT @ q.abs()).view(-1, G, n, 64).sum(1) + u * r["dk"].abs() + z
+    return r["dq"], b_dq, r["dk"], b_dk
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 3), (4, 2), (10, 1)])
+@pytest.mark.parametrize("w,sinks", [(1, 1), (1, 2), (1, 4), (0, 1), (0, 3), (5, 2), (1, 0), (27, 4), (0, 31)])
+def test_gradients_of_rows_that_see_few_keys(dtype, Hq, Hkv, w, sinks):
+    """Up to 32 keys a row, sinks among them, whatever the number of heads a
+    group: dP and delta nearly cancel, and the rounding of out is no part of
+    the error."""
+    lens = [900, 1, 333]
+    g = torch.Generator().manual_seed(w + 10 * sinks + Hq)
+    q, k, v, do = (torch.randn(sum(lens), h, 64, generator=g).to(DT[dtype]).cuda() for h in (Hq, Hkv, Hkv, Hq))
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    do2 = do.view(sum(lens), Hq * 64)
+    out, lse = lf.lf_window_attention_forward(q, k, v, w, sinks, cu_seqlens=cu)
+    dq, dk, _ = lf.lf_window_attention_backward(q, k, v, out, lse, do2, w, sinks, cu_seqlens=cu)
+    at = 0
+    for n in lens:
+        s = slice(at, at + n)
+        rq, bq, rk, bk = _bound_without_out(*(t[s].transpose(0, 1) for t in (q, k, v)), w, sinks, do[s].transpose(0, 1))
+        check("dq", dq[s].transpose(0, 1), rq, bq)
+        check("dk", dk[s].transpose(0, 1), rk, bk)
+        at += n
