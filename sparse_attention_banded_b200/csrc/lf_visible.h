@@ -142,6 +142,47 @@ LF_HD unsigned visible_bits32(int i, int c0, int n_keys, int w, int sinks) {
     return low_bits32(imin(i + 1, n_keys) - c0) & (~low_bits32(i - w - c0) | low_bits32(sinks - c0));
 }
 
+// ---- partial gradients of the sink keys -----------------------------------
+// The queries that see a sink from outside its window are cut into chunks of
+// `chunk` tokens of their sequence, of which those that hold only queries up
+// to w are skipped.  A sequence of at most w + 1 tokens has none; of the
+// others, `rows` rows a key/value head hold
+//   own(b, start) + key                the window's own contribution,
+//   chunk_row(b, start, k) + key       chunk k's,
+// for each sink key of the sequence.  `start` counts tokens over the batch (b
+// * L when padded), T in all.  No prefix sums: sequence b has the rows of
+// sequence b, or, where that is less, those of start / (w + 2) (sequences
+// that long are at least w + 2 apart), or those of its own tokens; its chunks
+// after the first have the slots from start / chunk on, since there are at
+// most n / chunk of them.
+struct SinkRows {
+    int sinks, w, chunk, how;
+    long long one;   // rows of the windows, and of the first chunks
+    long long rows;  // in all
+    LF_HD bool any(int n) const { return n > w + 1; }
+    LF_HD int first_chunk() const { return (w + 1) / chunk; }
+    LF_HD long long own(int b, int start) const {
+        return how == 0 ? (long long)b * sinks : how == 1 ? (long long)(start / (w + 2)) * sinks : start;
+    }
+    LF_HD long long chunk_row(int b, int start, int k) const {
+        k -= first_chunk();
+        return k == 0 ? one + own(b, start) : 2 * one + (long long)(start / chunk + k - 1) * sinks;
+    }
+};
+inline SinkRows sink_rows(int n_seqs, long long T, int w, int sinks, int chunk) {
+    SinkRows r = {sinks, w, chunk, 0, (long long)n_seqs * sinks, 0};
+    if (T / (w + 2) * sinks < r.one) {
+        r.how = 1;
+        r.one = T / (w + 2) * sinks;
+    }
+    if (T < r.one) {
+        r.how = 2;
+        r.one = T;
+    }
+    r.rows = 2 * r.one + T / chunk * sinks;
+    return r;
+}
+
 // ---- paged cache ----------------------------------------------------------
 // The page of key position j in a sequence's table row, -1 where the table
 // has none: past its width, or an entry outside [0, num_pages).

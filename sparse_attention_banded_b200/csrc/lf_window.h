@@ -31,17 +31,16 @@ struct WindowArgs {
     lf_heads dq, dk, dv;
     float* delta;       // [B][Hq][L] workspace
     float* part;        // partial gradients of the sink keys, see below
-    int chunk;          // tokens of one sink chunk
+    SinkRows sink;      // (sink.chunk: tokens of one chunk)
     int heads_group() const { return Hq / Hkv; }
     bool packed() const { return cu != nullptr; }
 };
 
-// Gradients of the sink keys: the queries that see a sink from outside its
-// window are cut into chunks of `chunk` tokens; chunk slot c (numbered as
-// token_tile numbers tiles) leaves its sum in
-//     part[n_seqs + c][kv head][key < sinks][dk, dv][64]
-// and the window's own contribution goes to part[sequence].  A last kernel
-// adds them in a fixed order and rounds once.
+// Gradients of the sink keys: chunks of queries leave their sums in
+//     part[kv head][row + key][dk, dv][64]
+// at the rows that SinkRows gives them, and the window's own contribution
+// goes there too (straight to dk and dv in sequences that have no chunk).  A
+// last kernel adds them in a fixed order and rounds once.
 // Chunks as long as an item of the window, which adds the fewest partials
 // and starts; shorter, for two items per SM, only where the window's items
 // (of 128 keys) leave SMs idle.  (Short ones everywhere: 536 us instead of
@@ -53,10 +52,8 @@ inline int sink_chunk(bool packed, int n_seqs, int Hkv, int L, int w) {
     if (rows / 128 >= 296 || share > most) return (int)most;
     return (int)(share < 64 ? 64 : share);
 }
-LF_HD size_t sink_part_floats(int Hkv, int sinks) { return (size_t)Hkv * sinks * 2 * 64; }
-inline size_t sink_slots(const WindowArgs& a) {
-    return (size_t)a.n_seqs + token_slots(a.packed(), a.n_seqs, a.L, a.chunk);
-}
+// Floats of `part`.
+inline size_t sink_part_floats(const SinkRows& r, int Hkv) { return (size_t)r.rows * Hkv * 2 * 64; }
 
 lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream);   // fp32
 lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream);  // fp32

@@ -65,7 +65,7 @@ lf_status window_args(const lf_heads* q, const lf_heads* k, const lf_heads* v, c
     a->L = L;
     a->w = imin(w, imax(L - 1, 0));
     a->sinks = a->w >= L - 1 ? 0 : imin(sinks, L);  // a full window holds every sink
-    a->chunk = sink_chunk(cu != nullptr, n_seqs, Hkv, L, a->w);
+    a->sink = sink_rows(n_seqs, (long long)B * L, a->w, a->sinks, sink_chunk(cu != nullptr, n_seqs, Hkv, L, a->w));
     a->scale = scale;
     a->dtype = dtype;
     return LF_OK;
@@ -134,8 +134,9 @@ size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int 
     if (check_window_sizes(packed, n_seqs, Hq, Hkv, L, w, sinks) != LF_OK || L == 0) return 0;
     size_t n = align256((size_t)(packed ? 1 : n_seqs) * Hq * L * sizeof(float));  // delta
     if (w < L - 1 && sinks > 0) {
-        const size_t slots = (size_t)n_seqs + token_slots(packed != 0, n_seqs, L, sink_chunk(packed != 0, n_seqs, Hkv, L, w));
-        n += align256(slots * sink_part_floats(Hkv, imin(sinks, L)) * sizeof(float));
+        const SinkRows r = sink_rows(n_seqs, (packed ? 1LL : n_seqs) * L, w, imin(sinks, L),
+                                     sink_chunk(packed != 0, n_seqs, Hkv, L, w));
+        n += align256(sink_part_floats(r, Hkv) * sizeof(float));
     }
     return n;
 }

@@ -283,16 +283,18 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
     float *K = sm, *V = K + kTile, *Q = V + kTile, *dO = Q + kTile, *P = dO + kTile, *S = P + kTile;
     __shared__ float lse_s[kT], delta_s[kT];
     const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
-    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.chunk : kT, blockIdx.x);
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.sink.chunk : kT, blockIdx.x);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (kSink ? t.t0 >= t.n : t.t0 >= t.rows) return;
+    const int n_sink = a.sink.any(t.n) ? imin(a.sinks, t.n) : 0;  // keys whose gradients have partials
+    if (kSink && (n_sink == 0 || t.t0 / a.sink.chunk < a.sink.first_chunk())) return;
     const int c0 = kSink ? blockIdx.z * kT : t.t0;
-    const int n_keys = kSink ? imin(t.n, a.sinks) : t.n;
+    const int n_keys = kSink ? n_sink : t.n;
     // query tokens: [q0, q1)
     int q0, q1;
     if (kSink) {
         q0 = imax(t.t0, a.w + 1);
-        q1 = imin(t.t0 + a.chunk, t.n);
+        q1 = imin(t.t0 + a.sink.chunk, t.n);
     } else {
         q0 = c0;
         q1 = (int)min((long long)t.n, (long long)c0 + kT + a.w);
@@ -344,23 +346,21 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
         tile_nn(dv, P, dO, ty, tx);
         tile_nn(dk, S, Q, ty, tx);
     }
+    const int seq_start = a.cu ? t.start : t.b * a.L;
+    const long long part_row =
+        kSink ? a.sink.chunk_row(t.b, seq_start, t.t0 / a.sink.chunk) : a.sink.own(t.b, seq_start);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int key = c0 + 4 * ty + i;
 #pragma unroll
         for (int c = 0; c < 4; ++c) dk[i][c] *= a.scale;
-        if (kSink || key < a.sinks) {
-            if (key >= (kSink ? a.sinks : imin(a.sinks, t.n))) {
-                if (kSink || key >= t.rows) continue;
-            } else {
-                const size_t slot = kSink ? a.n_seqs + blockIdx.x : t.b;
-                float* p = a.part + ((slot * a.Hkv + hk) * a.sinks + key) * 2 * kD + 4 * tx;
-                store4(p, dk[i]);
-                store4(p + kD, dv[i]);
-                continue;
-            }
+        if (key < n_sink) {
+            float* p = a.part + ((size_t)hk * a.sink.rows + part_row + key) * 2 * kD + 4 * tx;
+            store4(p, dk[i]);
+            store4(p + kD, dv[i]);
+            continue;
         }
-        if (key >= t.rows) continue;
+        if (kSink || key >= t.rows) continue;
         store4(view_row(a.dk, t.batch, hk, t.start + key) + 4 * tx, dk[i]);
         store4(view_row(a.dv, t.batch, hk, t.start + key) + 4 * tx, dv[i]);
     }
@@ -373,14 +373,16 @@ __global__ void __launch_bounds__(128) sink_reduce_kernel(const __grid_constant_
     const int key = blockIdx.x % a.sinks, hk = blockIdx.y, b = blockIdx.x / a.sinks, e = threadIdx.x;
     const int start = a.cu ? iclamp(a.cu[b], 0, a.L) : 0;
     const int n = a.cu ? iclamp(a.cu[b + 1], 0, a.L) - start : (a.lens ? iclamp(a.lens[b], 0, a.L) : a.L);
-    if (key >= n) return;
-    const size_t step = sink_part_floats(a.Hkv, a.sinks);
-    const float* p = a.part + ((size_t)hk * a.sinks + key) * 2 * kD + e;
-    float s = p[b * step];
-    const int first = a.cu ? start / a.chunk + b : b * ((a.L + a.chunk - 1) / a.chunk);
-    const int chunks = (n + a.chunk - 1) / a.chunk;
+    if (key >= n || !a.sink.any(n)) return;
+    const int seq_start = a.cu ? start : b * a.L;
+    const float* p = a.part + ((size_t)hk * a.sink.rows + key) * 2 * kD + e;
+    auto at = [&](long long row) { return p[(size_t)row * 2 * kD]; };
+    float s = at(a.sink.own(b, seq_start));
+    const int first = a.sink.first_chunk(), end = (n - 1) / a.sink.chunk + 1;
+    s += at(a.sink.chunk_row(b, seq_start, first));
+    const long long next = first + 1 < end ? a.sink.chunk_row(b, seq_start, first + 1) : 0;
 #pragma unroll 16
-    for (int c = 0; c < chunks; ++c) s += p[(size_t)(a.n_seqs + first + c) * step];
+    for (int c = 0; c < end - first - 1; ++c) s += at(next + (long long)c * a.sinks);
     const lf_heads& v = e < kD ? a.dk : a.dv;
     static_cast<T*>(v.data)[(a.cu ? 0 : b) * v.batch_stride + hk * v.head_stride + (start + key) * v.token_stride +
                             (e & (kD - 1))] = from_f<T>(s);
@@ -415,7 +417,7 @@ lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream) 
         st = launch(dkv_kernel<false>, dim3(token_slots(a.packed(), a.n_seqs, a.L, kT), a.Hkv), 6, a, stream);
     if (st == LF_OK && a.sinks > 0) {
         st = launch(dkv_kernel<true>,
-                    dim3(token_slots(a.packed(), a.n_seqs, a.L, a.chunk), a.Hkv, (a.sinks + kT - 1) / kT), 6, a, stream);
+                    dim3(token_slots(a.packed(), a.n_seqs, a.L, a.sink.chunk), a.Hkv, (a.sinks + kT - 1) / kT), 6, a, stream);
         if (st == LF_OK) st = launch_sink_reduce(a, stream);
     }
     return st;

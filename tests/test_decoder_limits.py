@@ -3,6 +3,7 @@ the library, sizes at the ends of their ranges, and the memory that a call
 asks for."""
 import ctypes
 import enum
+import random
 import subprocess
 import time
 
@@ -30,6 +31,14 @@ void plan(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int* o
 void slot(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int b, int start, int t, int* o) {
     PagedPlan p = paged_plan(n, Hq, Hkv, T, mq, width, w, s);
     o[0] = p.decode_slot(b, start, t); o[1] = p.decode_tokens;
+}
+void sink_layout(int n, long long T, int w, int s, int chunk, long long* o) {
+    SinkRows r = sink_rows(n, T, w, s, chunk);
+    o[0] = r.rows; o[1] = r.how; o[2] = r.first_chunk();
+}
+long long sink_row(int n, long long T, int w, int s, int chunk, int b, int start, int len, int k) {
+    SinkRows r = sink_rows(n, T, w, s, chunk);
+    return !r.any(len) ? -1 : k < 0 ? r.own(b, start) : r.chunk_row(b, start, k);
 }
 }
 '''
@@ -188,3 +197,63 @@ def test_too_many_pieces_are_refused_before_anything_runs(Hq, max_q):
     call = lambda n: lf.lib().lf_paged_attention_forward(  # noqa: E731
         heads(), heads(), heads(), p, p, p, n, Hq, 1024, 1000, max_q, 64, 64, 16, 100, 0, 0.125, 1, p, 1 << 45, None, p)
     assert call(1 << 20) == 13
+
+
+def _sink_rows(P, lens, starts, T, w, s, chunk):
+    """Every partial row that the gradients of the sink keys use, checked to
+    be used once and to lie inside; returns the rows in all."""
+    ll = ctypes.c_longlong
+    P.sink_row.restype = ll
+    o = (ll * 3)()
+    n = len(lens)
+    P.sink_layout(n, ll(T), w, s, chunk, o)
+    rows, how, first = o
+    seen = set()
+    for b, m in enumerate(lens):
+        # the chunks that hold a query past w, by enumeration
+        want = sorted({i // chunk for i in range(w + 1, m)})
+        assert not want or want[0] == first
+        for k in [-1] + want if want else []:
+            r = P.sink_row(n, ll(T), w, s, chunk, b, starts[b], m, k)
+            for key in range(min(s, m)):
+                assert 0 <= r + key < rows and (r + key) not in seen, (b, m, k, key)
+                seen.add(r + key)
+        if not want:
+            assert P.sink_row(n, ll(T), w, s, chunk, b, starts[b], m, 0) == -1
+    return rows, how
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_sink_partials_are_apart_and_inside(P, seed):
+    r = random.Random(seed)
+    lens = [r.choice([0, 1, 2, r.randint(0, 20), r.randint(0, 90), r.randint(0, 700)]) for _ in range(r.randint(1, 30))]
+    w, s = r.choice([0, 1, 5, 16, 63, 64, 200]), r.choice([1, 4, 33, 70])
+    chunk = r.choice([64, 128, 512])
+    if seed % 2:
+        T = sum(lens) + r.choice([0, 7])
+        starts = [sum(lens[:b]) for b in range(len(lens))]
+    else:  # padded
+        L = max(lens + [1])
+        T, starts = len(lens) * L, [b * L for b in range(len(lens))]
+    rows, how = _sink_rows(P, lens, starts, T, w, s, chunk)
+    assert rows <= 2 * min(len(lens) * s, T, T // (w + 2) * s) + T // chunk * s
+
+
+def test_sink_partials_take_each_way(P):
+    ways = set()
+    for lens, w, s in (([300, 20], 5, 4), ([30, 2, 1] * 30, 25, 4), ([20, 1, 0, 2] * 40, 2, 33)):
+        starts = [sum(lens[:b]) for b in range(len(lens))]
+        ways.add(_sink_rows(P, lens, starts, sum(lens), w, s, 64)[1])
+    assert ways == {0, 1, 2}
+
+
+def test_workspace_of_many_short_documents():
+    """4096 documents in 65536 tokens, 8 key heads, 64 sinks, window 256: no
+    more than 254 of them can reach past the window, and 128 chunks of 512
+    follow a first one: (2 * 254 + 128) * 64 rows of 512 bytes a head."""
+    got = lf.lf_window_attention_backward_workspace_bytes(True, 4096, 8, 8, 65536, 256, 64)
+    delta = 8 * 65536 * 4
+    assert got <= delta + (2 * 254 + 128) * 64 * 8 * 512 + 256
+    # and the usual call pays for its sinks alone
+    assert lf.lf_window_attention_backward_workspace_bytes(False, 1, 12, 12, 16384, 256, 32) <= \
+        12 * 16384 * 4 + (2 + 32) * 32 * 12 * 512 + 256

@@ -92,3 +92,34 @@ def test_gradients_of_rows_that_see_few_keys(dtype, Hq, Hkv, w, sinks):
         check("dq", dq[s].transpose(0, 1), rq, bq)
         check("dk", dk[s].transpose(0, 1), rk, bk)
         at += n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lens,w,sinks", [
+    ([300, 20, 700, 7], 5, 4),                 # partials numbered by sequence
+    ([30, 2, 1, 26, 27, 0] * 30 + [650], 25, 4),  # by start / (w + 2)
+    ([20, 1, 0, 2, 3, 4, 5] * 20, 2, 33),      # by token
+    ([150] * 5, 140, 130),                     # chunks that hold queries of the window only
+    ([64, 64], 63, 2)])                        # no query outside the window
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (5, 5)])
+def test_sink_gradients_of_many_sequences(dtype, lens, w, sinks, Hq, Hkv):
+    """Every partial is written before it is read, and none past the
+    workspace's end: it holds NaN before, and what follows it stays."""
+    g = torch.Generator().manual_seed(len(lens) + w)
+    T, tail = sum(lens), 3
+    q, k, v, do = (torch.randn(T + tail, h, 64, generator=g).to(DT[dtype]).cuda() for h in (Hq, Hkv, Hkv, Hq))
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    need = lf.lf_window_attention_backward_workspace_bytes(True, len(lens), Hq, Hkv, T + tail, w, sinks)
+    buf = torch.full((need + 65536,), 255, dtype=torch.uint8, device="cuda")
+    out, lse = lf.lf_window_attention_forward(q, k, v, w, sinks, cu_seqlens=cu)
+    got = lf.lf_window_attention_backward(q, k, v, out, lse, do.view(T + tail, -1), w, sinks, cu_seqlens=cu,
+                                          workspace=buf[:need])
+    assert bool((buf[need:] == 255).all())
+    at = 0
+    for n in lens:
+        if n:
+            s = slice(at, at + n)
+            r = reference(*(t[s].transpose(0, 1) for t in (q, k, v)), 0, w, sinks, 0.125, do[s].transpose(0, 1))
+            for name, t in zip(("dq", "dk", "dv"), got):
+                check(name, t[s].transpose(0, 1), r[name], r["b_" + name])
+        at += n
