@@ -32,6 +32,17 @@ lf_status check_view(const lf_heads* in, lf_heads* v, int batches, int heads, in
     return LF_OK;
 }
 
+// w and sinks clamped to sequences of at most L tokens, with the same keys
+// visible: a full window holds every sink, and L - 1 sinks hold every key
+// below the last.
+struct Visible {
+    int w, sinks;
+};
+Visible clamp_visible(int L, int w, int sinks) {
+    const int last = imax(L - 1, 0);
+    return w >= last || sinks >= last ? Visible{last, 0} : Visible{w, sinks};
+}
+
 lf_status check_window_sizes(int packed, int n_seqs, int Hq, int Hkv, int L, int w, int sinks) {
     if (n_seqs <= 0 || Hq <= 0 || Hkv <= 0 || L < 0 || w < 0 || sinks < 0) return LF_ERR_BAD_DIM;
     if (Hq % Hkv != 0 || Hq / Hkv > 64) return LF_ERR_BAD_DIM;
@@ -39,7 +50,7 @@ lf_status check_window_sizes(int packed, int n_seqs, int Hq, int Hkv, int L, int
     if (batches * Hq >= kInt31 || (L > 0 && batches * Hq > (kInt31 - 1) / L)) return LF_ERR_TOO_LARGE;
     if (L >= kMostPositions) return LF_ERR_TOO_LARGE;
     if (n_seqs >= (1 << 23) || Hkv > 65535) return LF_ERR_TOO_LARGE;
-    if ((long long)n_seqs * (sinks < L ? sinks : L) >= kInt31) return LF_ERR_TOO_LARGE;
+    if ((long long)n_seqs * clamp_visible(L, w, sinks).sinks >= kInt31) return LF_ERR_TOO_LARGE;
     return LF_OK;
 }
 
@@ -63,8 +74,9 @@ lf_status window_args(const lf_heads* q, const lf_heads* k, const lf_heads* v, c
     a->Hq = Hq;
     a->Hkv = Hkv;
     a->L = L;
-    a->w = imin(w, imax(L - 1, 0));
-    a->sinks = a->w >= L - 1 ? 0 : imin(sinks, L);  // a full window holds every sink
+    const Visible vis = clamp_visible(L, w, sinks);
+    a->w = vis.w;
+    a->sinks = vis.sinks;
     a->sink = sink_rows(n_seqs, (long long)B * L, a->w, a->sinks, sink_chunk(cu != nullptr, n_seqs, Hkv, L, a->w));
     a->scale = scale;
     a->dtype = dtype;
@@ -133,9 +145,10 @@ lf_status lf_window_attention_forward(const lf_heads* q, const lf_heads* k, cons
 size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int Hq, int Hkv, int L, int w, int sinks) {
     if (check_window_sizes(packed, n_seqs, Hq, Hkv, L, w, sinks) != LF_OK || L == 0) return 0;
     size_t n = align256((size_t)(packed ? 1 : n_seqs) * Hq * L * sizeof(float));  // delta
-    if (w < L - 1 && sinks > 0) {
-        const SinkRows r = sink_rows(n_seqs, (packed ? 1LL : n_seqs) * L, w, imin(sinks, L),
-                                     sink_chunk(packed != 0, n_seqs, Hkv, L, w));
+    const Visible vis = clamp_visible(L, w, sinks);
+    if (vis.sinks > 0) {
+        const SinkRows r = sink_rows(n_seqs, (packed ? 1LL : n_seqs) * L, vis.w, vis.sinks,
+                                     sink_chunk(packed != 0, n_seqs, Hkv, L, vis.w));
         n += align256(sink_part_floats(r, Hkv) * sizeof(float));
     }
     return n;

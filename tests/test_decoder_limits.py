@@ -257,3 +257,15 @@ def test_workspace_of_many_short_documents():
     # and the usual call pays for its sinks alone
     assert lf.lf_window_attention_backward_workspace_bytes(False, 1, 12, 12, 16384, 256, 32) <= \
         12 * 16384 * 4 + (2 + 32) * 32 * 12 * 512 + 256
+
+
+def test_sinks_that_hold_the_whole_sequence_need_no_partials():
+    """Every key below the query's is a sink: plain causal attention."""
+    size = lambda L, w, s: lf.lf_window_attention_backward_workspace_bytes(False, 2, 4, 4, L, w, s)  # noqa: E731
+    for L in (2, 100, 4096):
+        for s in (L - 1, L, L + 1, (1 << 31) - 1):
+            assert size(L, 0, s) == size(L, L, 0) <= 2 * 4 * L * 4 + 255
+    # (packed: 40000 sequences in 65536 tokens, whose product would pass 2^31)
+    packed = lambda w, s: lf.lf_window_attention_backward_workspace_bytes(True, 40000, 4, 4, 65536, w, s)  # noqa: E731
+    assert packed(5, 65536) == packed(65536, 100000) == packed(65536, 0) == 4 * 65536 * 4
+    assert packed(5, 65534) == 0  # too large

@@ -123,3 +123,24 @@ def test_sink_gradients_of_many_sequences(dtype, lens, w, sinks, Hq, Hkv):
             for name, t in zip(("dq", "dk", "dv"), got):
                 check(name, t[s].transpose(0, 1), r[name], r["b_" + name])
         at += n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("sinks", [298, 299, 300, 301, (1 << 31) - 1])
+def test_sinks_up_to_every_key(dtype, sinks):
+    """From L - 1 sinks on the attention is plainly causal: the same bits as
+    a window of that length, forward and backward."""
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(2, h, 300, 64, generator=g).to(DT[dtype]).cuda() for h in (4, 2, 2))
+    do = torch.randn(2, 300, 256, generator=g).to(DT[dtype]).cuda()
+    out, lse = lf.lf_window_attention_forward(q, k, v, 3, sinks)
+    got = lf.lf_window_attention_backward(q, k, v, out, lse, do, 3, sinks)
+    for b in range(2):
+        r = reference(q[b], k[b], v[b], 0, 3, sinks, 0.125, do[b].view(300, 4, 64).transpose(0, 1))
+        check("out", out[b].view(300, 4, 64).transpose(0, 1), r["out"], r["b_out"])
+        for name, t in zip(("dq", "dk", "dv"), got):
+            check(name, t[b], r[name], r["b_" + name])
+    if sinks >= 299:
+        out2, lse2 = lf.lf_window_attention_forward(q, k, v, 300, 0)
+        want = lf.lf_window_attention_backward(q, k, v, out2, lse2, do, 300, 0)
+        assert torch.equal(out, out2) and all(torch.equal(a, b) for a, b in zip(got, want))
