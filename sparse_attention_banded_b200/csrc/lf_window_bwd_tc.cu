@@ -425,7 +425,8 @@ __device__ __forceinline__ bool key_item(const WindowArgs& a, int item, int sink
         p.chunk = t.t0 / a.sink.chunk;
         if (p.n_sink == 0 || p.chunk < a.sink.first_chunk()) return false;
         p.c0 = at / sink_slots * 128;
-        p.q0 = imax(t.t0, imin(p.c0, t.n) + a.w + 1);
+        if (p.c0 >= p.n_sink) return false;  // (more sinks than the sequence has)
+        p.q0 = imax(t.t0, p.c0 + a.w + 1);
         p.q1 = imin(t.t0 + a.sink.chunk, t.n);
         p.n_keys = p.n_sink;
     } else {

@@ -276,19 +276,21 @@ __global__ void __launch_bounds__(kThreads) dq_kernel(const __grid_constant__ Wi
 // ---------------------------------------------------------------- dK, dV
 // kSink false: one block of 64 keys over the queries that hold it in their
 // window.  kSink true: one block of sink keys over a chunk of the queries
-// that see it from outside their window; writes fp32 partial sums.
+// that see it from outside their window; writes fp32 partial sums.  blockIdx.x
+// counts `slots` tiles of keys, or of queries for each block of sink keys.
 template <bool kSink>
-__global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ WindowArgs a) {
+__global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ WindowArgs a, int slots) {
     extern __shared__ float sm[];
     float *K = sm, *V = K + kTile, *Q = V + kTile, *dO = Q + kTile, *P = dO + kTile, *S = P + kTile;
     __shared__ float lse_s[kT], delta_s[kT];
     const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
-    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.sink.chunk : kT, blockIdx.x);
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.sink.chunk : kT, blockIdx.x % slots);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (kSink ? t.t0 >= t.n : t.t0 >= t.rows) return;
     const int n_sink = a.sink.any(t.n) ? imin(a.sinks, t.n) : 0;  // keys whose gradients have partials
     if (kSink && (n_sink == 0 || t.t0 / a.sink.chunk < a.sink.first_chunk())) return;
-    const int c0 = kSink ? blockIdx.z * kT : t.t0;
+    const int c0 = kSink ? (int)(blockIdx.x / slots) * kT : t.t0;
+    if (kSink && c0 >= n_sink) return;  // (more sinks than the sequence has)
     const int n_keys = kSink ? n_sink : t.n;
     // query tokens: [q0, q1)
     int q0, q1;
@@ -394,12 +396,12 @@ lf_status set_smem(K kernel, size_t bytes) {
                ? LF_OK : LF_ERR_CUDA;
 }
 
-template <typename K, typename A>
-lf_status launch(K kernel, dim3 grid, int tiles, const A& a, cudaStream_t stream) {
+template <typename K, typename... A>
+lf_status launch(K kernel, dim3 grid, int tiles, cudaStream_t stream, const A&... a) {
     const size_t bytes = (size_t)tiles * kTile * sizeof(float);
     lf_status st = set_smem(kernel, bytes);
     if (st != LF_OK) return st;
-    kernel<<<grid, kThreads, bytes, stream>>>(a);
+    kernel<<<grid, kThreads, bytes, stream>>>(a...);
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
@@ -407,17 +409,18 @@ lf_status launch(K kernel, dim3 grid, int tiles, const A& a, cudaStream_t stream
 
 lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream) {
     const int TQ = kT / a.heads_group();
-    return launch(forward_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 4, a, stream);
+    return launch(forward_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 4, stream, a);
 }
 
 lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream) {
-    const int TQ = kT / a.heads_group();
-    lf_status st = launch(dq_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 5, a, stream);
-    if (st == LF_OK)
-        st = launch(dkv_kernel<false>, dim3(token_slots(a.packed(), a.n_seqs, a.L, kT), a.Hkv), 6, a, stream);
+    const int TQ = kT / a.heads_group(), tiles = token_slots(a.packed(), a.n_seqs, a.L, kT);
+    const int chunks = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.sink.chunk) : 0;
+    const long long sink_tiles = (long long)chunks * ((a.sinks + kT - 1) / kT);
+    if (sink_tiles > INT32_MAX) return LF_ERR_TOO_LARGE;
+    lf_status st = launch(dq_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 5, stream, a);
+    if (st == LF_OK) st = launch(dkv_kernel<false>, dim3(tiles, a.Hkv), 6, stream, a, tiles);
     if (st == LF_OK && a.sinks > 0) {
-        st = launch(dkv_kernel<true>,
-                    dim3(token_slots(a.packed(), a.n_seqs, a.L, a.sink.chunk), a.Hkv, (a.sinks + kT - 1) / kT), 6, a, stream);
+        st = launch(dkv_kernel<true>, dim3((unsigned)sink_tiles, a.Hkv), 6, stream, a, chunks);
         if (st == LF_OK) st = launch_sink_reduce(a, stream);
     }
     return st;

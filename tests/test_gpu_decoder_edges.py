@@ -144,3 +144,41 @@ def test_sinks_up_to_every_key(dtype, sinks):
         out2, lse2 = lf.lf_window_attention_forward(q, k, v, 300, 0)
         want = lf.lf_window_attention_backward(q, k, v, out2, lse2, do, 300, 0)
         assert torch.equal(out, out2) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_sinks_far_wider_than_the_sequences(dtype):
+    """4.2 million sinks, short sequences, most of the packed rows in none."""
+    lens, T, w, sinks = [1000, 5, 130], 4300000, 2100000, 4200000
+    g = torch.Generator().manual_seed(4)
+    q, k, v, do = (torch.zeros(T, 1, 64, dtype=DT[dtype], device="cuda") for _ in range(4))
+    for t in (q, k, v, do):
+        t[:sum(lens)] = torch.randn(sum(lens), 1, 64, generator=g).to(DT[dtype]).cuda()
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    out, lse = lf.lf_window_attention_forward(q, k, v, w, sinks, cu_seqlens=cu)
+    got = lf.lf_window_attention_backward(q, k, v, out, lse, do.view(T, 64), w, sinks, cu_seqlens=cu)
+    at = 0
+    for n in lens:
+        s = slice(at, at + n)
+        r = reference(*(t[s].transpose(0, 1) for t in (q, k, v)), 0, w, sinks, 0.125, do[s].transpose(0, 1))
+        for name, t in zip(("dq", "dk", "dv"), got):
+            check(name, t[s].transpose(0, 1), r[name], r["b_" + name])
+        at += n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_sinks_than_keys_beyond_the_window(dtype):
+    """Several blocks of sinks, of which short sequences have the first alone."""
+    lens, w, sinks, Hq, Hkv = [700, 100, 60, 300, 129], 40, 400, 2, 1
+    g = torch.Generator().manual_seed(5)
+    q, k, v, do = (torch.randn(sum(lens), h, 64, generator=g).to(DT[dtype]).cuda() for h in (Hq, Hkv, Hkv, Hq))
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    out, lse = lf.lf_window_attention_forward(q, k, v, w, sinks, cu_seqlens=cu)
+    got = lf.lf_window_attention_backward(q, k, v, out, lse, do.view(-1, Hq * 64), w, sinks, cu_seqlens=cu)
+    at = 0
+    for n in lens:
+        s = slice(at, at + n)
+        r = reference(*(t[s].transpose(0, 1) for t in (q, k, v)), 0, w, sinks, 0.125, do[s].transpose(0, 1))
+        for name, t in zip(("dq", "dk", "dv"), got):
+            check(name, t[s].transpose(0, 1), r[name], r["b_" + name])
+        at += n
