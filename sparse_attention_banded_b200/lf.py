@@ -396,12 +396,18 @@ def _encoder(fn_name, size_fn, x, local_mask, global_mask, layers, H, w, attn_sc
 # --------------------------------------------------------------------------
 # windowed causal attention with sinks, its paged form, layer norm
 # --------------------------------------------------------------------------
+# stream: the torch.cuda.Stream to launch on (default: the current one).  New
+# outputs belong to it: a caller that uses them on another stream orders the
+# two and calls their record_stream.  The calls are no autograd functions:
+# gradients are the _backward calls' to compute.
 _HERE_ALREADY = contextlib.nullcontext()
 
 
 def _on(first, stream, *tensors):
     """A context in which the device of `first` is current and `stream` (if
-    given) the stream that outputs and workspaces are allocated on."""
+    given) the stream that outputs and workspaces are allocated on.  Where it
+    is not the current stream, the tensors are marked as used on it, so that
+    their memory waits for it when the caller lets go of them."""
     dev = first.get_device()
     if dev < 0:
         raise ValueError("expected a CUDA tensor")
@@ -411,6 +417,10 @@ def _on(first, stream, *tensors):
     if stream is not None:
         if stream.device != first.device:
             raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, first.device))
+        if stream != torch.cuda.current_stream(dev):
+            for t in (first, *tensors):
+                if t is not None:
+                    t.record_stream(stream)
         return torch.cuda.stream(stream)  # makes its device current too
     return _HERE_ALREADY if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 

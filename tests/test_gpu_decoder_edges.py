@@ -182,3 +182,59 @@ def test_more_sinks_than_keys_beyond_the_window(dtype):
         for name, t in zip(("dq", "dk", "dv"), got):
             check(name, t[s].transpose(0, 1), r[name], r["b_" + name])
         at += n
+
+
+def _calls_on_a_stream():
+    h = lambda *s: torch.randn(*s, device="cuda").half()  # noqa: E731
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def window(st):
+        q = h(2, 4, 300, 64)
+        return [q], lambda: lf.lf_window_attention_forward(q, q, q, 20, 2, stream=st)[0]
+
+    def backward(st):
+        q, do = h(2, 4, 300, 64), h(2, 300, 256)
+        out, lse = lf.lf_window_attention_forward(q, q, q, 20, 2)
+        return [do], lambda: lf.lf_window_attention_backward(q, q, q, out, lse, do, 20, 2, stream=st)[0]
+
+    def append(st):
+        k, c, table, cu, kv = h(300, 4, 64), h(40, 4, 16, 64), torch.arange(40, dtype=torch.int32, device="cuda")[None], i32(0, 300), i32(300)
+        return [k], lambda: (lf.lf_paged_cache_append(k, k, c, c, table, cu, kv, stream=st), c)[1]
+
+    def paged(st):
+        q, c, table, cu, kv = h(300, 4, 64), h(40, 4, 16, 64), torch.arange(40, dtype=torch.int32, device="cuda")[None], i32(0, 300), i32(300)
+        return [q], lambda: lf.lf_paged_attention_forward(q, c, c, table, cu, kv, 300, stream=st)
+
+    def norm(st):
+        x = h(500, 512)
+        return [x], lambda: lf.lf_layer_norm_forward(x, stream=st)[0]
+
+    def norm_backward(st):
+        x, dy = h(500, 512), h(500, 512)
+        _, mean, rstd = lf.lf_layer_norm_forward(x)
+        return [dy], lambda: lf.lf_layer_norm_backward(dy, x, None, mean, rstd, stream=st)[0]
+
+    return dict(window=window, backward=backward, append=append, paged=paged, norm=norm, norm_backward=norm_backward)
+
+
+@pytest.mark.parametrize("name", ["window", "backward", "append", "paged", "norm", "norm_backward"])
+def test_an_input_freed_before_the_other_stream_has_read_it(name):
+    """The caller lets go of an input while the call on another stream still
+    waits: its memory is not handed out again."""
+    side = torch.cuda.Stream()
+    inputs, call = _calls_on_a_stream()[name](side)
+    want = call().clone() if name != "append" else None
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # 0.1 s
+    got = call()
+    ptr, shape = inputs[0].data_ptr(), inputs[0].shape
+    if name == "append":
+        want = inputs[0].clone()
+    del call, inputs
+    new = [torch.full(shape, 7.0, dtype=torch.float16, device="cuda") for _ in range(4)]
+    assert ptr not in [t.data_ptr() for t in new]
+    torch.cuda.synchronize()
+    if name == "append":
+        got = got[:, :, :].transpose(1, 2).reshape(-1, 4, 64)[:300]
+    assert torch.equal(got, want)
