@@ -482,7 +482,9 @@ size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int 
  *     dq_i = s sum_j dS_ij k_j,   dk_j = s sum_i dS_ij q_i,
  * summed over the Hq / Hkv query heads of a key/value head.  P and dS are
  * rounded to dtype as tensor-core operands (LF_F32: not rounded); every sum
- * is fp32 and has a fixed order, so results repeat bit for bit.
+ * is fp32 and has a fixed order, so results repeat bit for bit.  LF_F16: dS
+ * is of the size of dout times P, and loses bits below 2^-14; scale the loss
+ * so that dout is of order one (or use LF_BF16).
  *   out, lse   as the forward call wrote them;  dout [B, L, Hq * 64], dense
  *   dq, dk, dv views like q, k, v, written in full (rows past a sequence's
  *              tokens as the forward call's out: left, or zeros)

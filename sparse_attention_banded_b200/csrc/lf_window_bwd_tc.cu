@@ -26,7 +26,10 @@
 // packed tokens, 16 / 4 heads, window 1024, bf16: dQ 153 us, dK and dV 241;
 // 16384 tokens, 12 heads, window 256, 32 sinks, fp16: 73 and 99.  P and dS
 // are rounded to the storage type, the MMA's operand type; accumulators are
-// fp32, rounded once.
+// fp32, rounded once.  dS is about |dout| P: fp16 keeps its bits where the
+// loss is scaled so that dout is of order one, as fp16 training does (errors of
+// dQ in those of gradients rounded once, window 1024: dout of order 1 1.45,
+// 1e-3 3.0, 1e-4 3.6; bf16 has the range).
 //
 // Rows of other sequences (or of no token) that a tile's loads bring along
 // are zeroed in shared memory where they are a product's inner dimension:
@@ -392,6 +395,15 @@ dq_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs 
 }
 
 // ---------------------------------------------------------------- dK, dV
+// P is an operand of dV as P 2^kLift: of rows that see more than 2^14 keys, P
+// would fall among fp16's subnormal numbers (1 / 48000 is off by 2^-10 there).
+// Lifted, it keeps its bits down to 2^-24, and stays finite up to 2^6 (scores
+// that large lose bits in fp32 first).  The lift is part of the exponent's
+// offset and of the factor of dP - delta, so it costs no instruction but the
+// last products of dV.
+template <typename T>
+constexpr int kLift = MmaFormat<T>::fmt == 0 ? 10 : 0;
+
 // What the roles need to know of an item: 128 keys and the query tokens
 // [q0, q1) that its dK and dV sum over.  nq: steps; 0: rows of zeros
 // (padding, or a chunk inside every window), < 0: no more items.
@@ -455,6 +467,7 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
     pdl_launch_dependents();
     pdl_wait();
     const int G = a.Hq / a.Hkv, TQ = 64 / G;
+    constexpr float kDrop = 1.0f / (1 << kLift<T>);
     [[maybe_unused]] KeyItem own;
     if constexpr (!kMany) {
         if (!key_item(a, blockIdx.x, sink_slots, sink_items, per_head, TQ, own)) return;
@@ -466,7 +479,7 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
     }
     const Ctx c = setup(smem, warp, lane);
     const uint32_t tmS = c.tmem, tmP = c.tmem + 64, tmV = c.tmem + 128, tmK = c.tmem + 192;
-    float* row_s = reinterpret_cast<float*>(smem + kOffRow);  // [stage][-lse log2e, -delta][64]
+    float* row_s = reinterpret_cast<float*>(smem + kOffRow);  // [stage][kLift - lse log2e, -delta kDrop][64]
     auto plan_slot = [&](int k) { return reinterpret_cast<KeyItem*>(smem + kOffPlan + (k % kRing) * kPlanBytes); };
     // The items, in order; the slot of item k - 1 is handed back when the
     // role asks for item k.  NULL at the end and after an abort.
@@ -522,8 +535,8 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
                     const int row = lane + 32 * u, tok = qt + row / G;
                     const bool live = row < TQ * G && tok < p.q1;
                     const size_t at = ((size_t)p.batch * a.Hq + p.hk * G + row % G) * a.L + p.start + tok;
-                    nl[u] = live ? -a.lse[at] * kLog2e : 0.0f;
-                    nd[u] = live ? -a.delta[at] : 0.0f;
+                    nl[u] = live ? fmaf(-a.lse[at], kLog2e, (float)kLift<T>) : 0.0f;
+                    nd[u] = live ? -a.delta[at] * kDrop : 0.0f;
                 }
                 ok = warp_wait(&c.b_empty[s], ((g / kStages) & 1) ^ 1, c.abort_flag);
                 if (!ok) break;
@@ -665,7 +678,7 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
                 ok = warp_wait(c.s_full, g & 1, c.abort_flag) && warp_wait(&c.b_full[s], (g / kStages) & 1, c.abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                // P, kept in fp32 for dS
+                // P 2^kLift, kept in fp32 for dS
                 float x[32];
                 uint32_t pk[16];
                 tmem_ld32f(tS, x);
@@ -712,8 +725,9 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const float4 nd = nd4[u];
-                    const float2 d0 = fmul2(make_float2(x[4 * u], x[4 * u + 1]), fadd2(make_float2(y[4 * u], y[4 * u + 1]), make_float2(nd.x, nd.y)));
-                    const float2 d1 = fmul2(make_float2(x[4 * u + 2], x[4 * u + 3]), fadd2(make_float2(y[4 * u + 2], y[4 * u + 3]), make_float2(nd.z, nd.w)));
+                    const float2 drop = make_float2(kDrop, kDrop);
+                    const float2 d0 = fmul2(make_float2(x[4 * u], x[4 * u + 1]), ffma2(make_float2(y[4 * u], y[4 * u + 1]), drop, make_float2(nd.x, nd.y)));
+                    const float2 d1 = fmul2(make_float2(x[4 * u + 2], x[4 * u + 3]), ffma2(make_float2(y[4 * u + 2], y[4 * u + 3]), drop, make_float2(nd.z, nd.w)));
                     y[4 * u] = d0.x;
                     y[4 * u + 1] = d0.y;
                     y[4 * u + 2] = d1.x;
@@ -741,9 +755,10 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
                     tmem_ld32f((w ? tmV : tmK) + lane_off + half * 32, o);
                     tmem_ld_wait();
                     regs_ready<32>(o);
-                    if (w == 0) {
+                    if (w == 0 || kLift<T> > 0) {
+                        const float f = w == 0 ? a.scale : kDrop;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= a.scale;
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
                     }
                     if (to.part) {
                         float4* d = reinterpret_cast<float4*>(to.part + w * kD);

@@ -238,3 +238,24 @@ def test_an_input_freed_before_the_other_stream_has_read_it(name):
     if name == "append":
         got = got[:, :, :].transpose(1, 2).reshape(-1, 4, 64)[:300]
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [33000, 48005, 65500])
+def test_dv_of_late_keys_in_a_long_context(dtype, n):
+    """q = 0: P is 1 / (i + 1), below fp16's 2^-14 in rows past 16384, and as
+    exact as in other rows.  The log-sum-exp is ln(i + 1) from an exact sum:
+    15.6 in log2, rounded three times at 2^-24 and off by 2^-22 from the
+    logarithm, so P is off by e = 2^-18 and by its rounding, u; the last 64
+    keys' sums have at most 64 terms (2^-18), and are rounded once:
+        (u + 2^-17) sum p |dout| + u |dv| + z."""
+    g = torch.Generator().manual_seed(n)
+    q = torch.zeros(1, 1, n, 64, dtype=DT[dtype], device="cuda")
+    k, v = (torch.randn(1, 1, n, 64, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    do = (8 + 8 * torch.rand(1, n, 64, generator=g)).to(DT[dtype]).cuda()
+    out, lse = lf.lf_window_attention_forward(q, k, v, n)
+    _, _, dv = lf.lf_window_attention_backward(q, k, v, out, lse, do, n)
+    p = 1 / torch.arange(n - 63, n + 1, dtype=torch.double, device="cuda")[:, None]
+    want = (p * do[0, -64:].double()).flip(0).cumsum(0).flip(0)
+    u, z = half_step(DT[dtype]), subnormal_half_step(DT[dtype])
+    check("dv", dv[0, 0, -64:], want, (2 * u + 2.0 ** -17) * want + z)  # (all terms are positive)
