@@ -483,11 +483,9 @@ def _int32(**values):
     return ints
 
 
-def _fits(name, *sizes):
-    """Refuses sizes that the C interface's int would cut off."""
-    for n in sizes:
-        if n >> 31:
-            raise ValueError("%s: size %d is not an int32" % (name, n))
+def _too_wide(*sizes):
+    """Sizes that the C interface's int would cut off are refused."""
+    raise ValueError("a size of %s is not an int32" % (sizes,))
 
 
 def _heads(name, t, shape=None, dtype=None):
@@ -511,7 +509,8 @@ def _window_shape(q, k, v, cu_seqlens, seq_lens):
     kv = k.shape
     if k.dtype is not dtype or v.dtype is not dtype or v.shape != kv or len(kv) != len(shape):
         raise ValueError("k, v: expected two [.., Hkv, .., 64] of %s like q, got %s and %s" % (dtype, tuple(kv), tuple(v.shape)))
-    _fits("q, k", *shape, kv[1])
+    if (shape[0] | shape[1] | shape[-2] | kv[1]) >> 31:
+        _too_wide(shape, kv)
     if packed:
         L, Hq, _ = shape
         Hkv = kv[1]
@@ -602,12 +601,13 @@ def _paged_shape(new, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
     if block_table.dim() != 2 or block_table.dtype is not i32:
         raise ValueError("block_table: expected [n_seqs, max_pages] int32")
     n, max_pages = block_table.shape
-    _fits("block_table", n, max_pages)
-    _fits("k_cache", *cache)
-    _fits("new tokens", new.shape[0], new.shape[1])
+    T, heads, _ = new.shape
+    num_pages, Hkv, page_size, _ = cache
+    if (n | max_pages | T | heads | num_pages | Hkv | page_size) >> 31:
+        _too_wide((n, max_pages), new.shape, cache)
     _want("cu_seqlens", cu_seqlens, i32, (n + 1,))
     _want("kv_lens", kv_lens, i32, (n,))
-    return n, new.shape[0], cache[1], max_pages, cache[0], cache[2]
+    return n, T, Hkv, max_pages, num_pages, page_size
 
 
 def lf_paged_cache_append(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, stream=None):
@@ -665,7 +665,8 @@ def _rows(name, t):
         raise ValueError("%s: expected [..., N]" % name)
     N = shape[-1]
     rows = t.numel() // N if N else 0
-    _fits(name, rows, N)
+    if (rows | N) >> 31:
+        _too_wide(shape)
     if t.is_contiguous():
         return t.data_ptr(), rows, N, N
     if len(shape) == 2 and (t.stride(1) == 1 or N == 1):
