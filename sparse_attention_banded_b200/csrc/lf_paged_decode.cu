@@ -249,10 +249,10 @@ decode_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ Paged
                 Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]), Pair<T>::pack(x[4], x[5]), Pair<T>::pack(x[6], x[7]));
         } else {
             const size_t at = ((size_t)piece * pl.decode_tokens + pl.decode_slot(b, start, r / G)) * a.Hq + head;
-            float4* d = reinterpret_cast<float4*>(pl.decode_o + at * kD + c);
+            float4* d = reinterpret_cast<float4*>(pl.decode_o() + at * kD + c);
             d[0] = make_float4(x[0], x[1], x[2], x[3]);
             d[1] = make_float4(x[4], x[5], x[6], x[7]);
-            if (c == 0) pl.decode_lse[at] = sum == 0.f ? -INFINITY : top + log2f(sum);
+            if (c == 0) pl.decode_lse(a.T, a.Hq)[at] = sum == 0.f ? -INFINITY : top + log2f(sum);
         }
     }
 }
@@ -312,15 +312,15 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Page
     size_t step, at0;
     if (pl.decode && n * G <= kRows) {
         pieces = (decode_tiles(first, n, kv, a.w, a.sinks).n + pl.chunk - 1) / pl.chunk;
-        po = pl.decode_o;
-        pe = pl.decode_lse;
+        po = pl.decode_o();
+        pe = pl.decode_lse(a.T, a.Hq);
         step = (size_t)pl.decode_tokens * a.Hq;
         at0 = (size_t)pl.decode_slot(b, start, tok - start) * a.Hq + h0;
     } else {
         const int TQ = 128 / G, t0 = (tok - start) / TQ * TQ;
         pieces = (tile_key_blocks(first, t0, imin(t0 + TQ, n), kv, a.w, a.sinks).n + pl.per - 1) / pl.per;
-        po = pl.o;
-        pe = pl.lse;
+        po = pl.o(a.Hq);
+        pe = pl.lse(a.T, a.Hq);
         step = (size_t)a.T * a.Hq;
         at0 = (size_t)tok * a.Hq + h0;
     }

@@ -16,30 +16,37 @@ constexpr int kDecodeRows = 16;
 
 struct PagedPlan {
     bool decode, tensor;  // kernels launched
+    bool ahead;           // few items: two CTAs per SM, worked on ahead
     int chunk;            // decode: tiles of 8 keys per CTA
     int decode_splits;    // pieces of a context (n_seqs times that: its gridDim.x)
     int per;              // tensor cores: blocks of 64 keys per CTA
     int tensor_splits;    // pieces of a tile, at most
-    bool ahead;           // few items: two CTAs per SM, worked on ahead
     // Partial rows of contexts in several pieces: normalised sums and their
     // log2-sum-exp.  The decode kernel cuts a context into far more pieces
-    // than the tensor cores do, of far fewer rows, so each has its own.
+    // than the tensor cores do, of far fewer rows, so each has its own:
+    //     [decode_splits][decode_tokens * Hq] and [tensor_splits][T * Hq]
+    // rows of 64, then the log2-sum-exps of both.  (One pointer: 32 bytes more
+    // of arguments are 0.4 us of a launch.)
     int decode_tokens;    // tokens that the decode kernel may work on
     int decode_each;      // of one sequence; 0: counted over the batch's tokens
-    float *decode_o, *decode_lse;  // [decode_splits][decode_tokens * Hq][64], [..]
-    float *o, *lse;                // [tensor_splits][T * Hq][64], [..]
-    // Items of the tensor-core kernel.
-    long long tensor_items(int T, int n_seqs, int Hkv, int G) const {
-        return tensor ? (long long)packed_slots(T, n_seqs, 128 / G) * Hkv * tensor_splits : 0;
-    }
+    float* part;
     LF_HD int splits() const { return imax(decode ? decode_splits : 1, tensor ? tensor_splits : 1); }
     // Where the decode kernel leaves the token t of sequence b, which starts at `start`.
     LF_HD int decode_slot(int b, int start, int t) const { return decode_each ? b * decode_each + t : start + t; }
-    size_t decode_rows(int Hq) const {
+    LF_HD size_t decode_rows(int Hq) const {
         return decode && decode_splits > 1 ? (size_t)decode_splits * decode_tokens * Hq : 0;
     }
-    size_t tensor_rows(int T, int Hq) const {
+    LF_HD size_t tensor_rows(int T, int Hq) const {
         return tensor && tensor_splits > 1 ? (size_t)tensor_splits * T * Hq : 0;
+    }
+    LF_HD size_t rows(int T, int Hq) const { return decode_rows(Hq) + tensor_rows(T, Hq); }
+    LF_HD float* decode_o() const { return part; }
+    LF_HD float* o(int Hq) const { return part + decode_rows(Hq) * 64; }
+    LF_HD float* decode_lse(int T, int Hq) const { return part + rows(T, Hq) * 64; }
+    LF_HD float* lse(int T, int Hq) const { return decode_lse(T, Hq) + decode_rows(Hq); }
+    // Items of the tensor-core kernel.
+    long long tensor_items(int T, int n_seqs, int Hkv, int G) const {
+        return tensor ? (long long)packed_slots(T, n_seqs, 128 / G) * Hkv * tensor_splits : 0;
     }
 };
 

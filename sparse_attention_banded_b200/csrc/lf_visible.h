@@ -156,32 +156,26 @@ LF_HD unsigned visible_bits32(int i, int c0, int n_keys, int w, int sinks) {
 // after the first have the slots from start / chunk on, since there are at
 // most n / chunk of them.
 struct SinkRows {
-    int sinks, w, chunk, how;
-    long long one;   // rows of the windows, and of the first chunks
-    long long rows;  // in all
+    int n_seqs, T, w, sinks, chunk;
     LF_HD bool any(int n) const { return n > w + 1; }
     LF_HD int first_chunk() const { return (w + 1) / chunk; }
+    LF_HD long long by_seq() const { return (long long)n_seqs * sinks; }
+    LF_HD long long by_start() const { return (long long)(T / (w + 2)) * sinks; }
+    // Rows of the windows, and of the first chunks.
+    LF_HD long long one() const {
+        const long long r = by_start() < by_seq() ? by_start() : by_seq();
+        return T < r ? T : r;
+    }
+    LF_HD long long rows() const { return 2 * one() + (long long)(T / chunk) * sinks; }
     LF_HD long long own(int b, int start) const {
-        return how == 0 ? (long long)b * sinks : how == 1 ? (long long)(start / (w + 2)) * sinks : start;
+        const long long r = one();
+        return r == by_seq() ? (long long)b * sinks : r == by_start() ? (long long)(start / (w + 2)) * sinks : start;
     }
     LF_HD long long chunk_row(int b, int start, int k) const {
         k -= first_chunk();
-        return k == 0 ? one + own(b, start) : 2 * one + (long long)(start / chunk + k - 1) * sinks;
+        return k == 0 ? one() + own(b, start) : 2 * one() + (long long)(start / chunk + k - 1) * sinks;
     }
 };
-inline SinkRows sink_rows(int n_seqs, long long T, int w, int sinks, int chunk) {
-    SinkRows r = {sinks, w, chunk, 0, (long long)n_seqs * sinks, 0};
-    if (T / (w + 2) * sinks < r.one) {
-        r.how = 1;
-        r.one = T / (w + 2) * sinks;
-    }
-    if (T < r.one) {
-        r.how = 2;
-        r.one = T;
-    }
-    r.rows = 2 * r.one + T / chunk * sinks;
-    return r;
-}
 
 // ---- paged cache ----------------------------------------------------------
 // The page of key position j in a sequence's table row, -1 where the table

@@ -31,9 +31,12 @@ struct WindowArgs {
     lf_heads dq, dk, dv;
     float* delta;       // [B][Hq][L] workspace
     float* part;        // partial gradients of the sink keys, see below
-    SinkRows sink;      // (sink.chunk: tokens of one chunk)
+    int chunk;          // tokens of one sink chunk
     int heads_group() const { return Hq / Hkv; }
     bool packed() const { return cu != nullptr; }
+    // (worked out where it is needed: 48 bytes more of arguments are 0.4 us of
+    // a launch)
+    LF_HD SinkRows sink() const { return {n_seqs, cu ? L : n_seqs * L, w, sinks, chunk}; }
 };
 
 // Gradients of the sink keys: chunks of queries leave their sums in
@@ -53,7 +56,7 @@ inline int sink_chunk(bool packed, int n_seqs, int Hkv, int L, int w) {
     return (int)(share < 64 ? 64 : share);
 }
 // Floats of `part`.
-inline size_t sink_part_floats(const SinkRows& r, int Hkv) { return (size_t)r.rows * Hkv * 2 * 64; }
+inline size_t sink_part_floats(const SinkRows& r, int Hkv) { return (size_t)r.rows() * Hkv * 2 * 64; }
 
 lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream);   // fp32
 lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream);  // fp32

@@ -77,7 +77,7 @@ lf_status window_args(const lf_heads* q, const lf_heads* k, const lf_heads* v, c
     const Visible vis = clamp_visible(L, w, sinks);
     a->w = vis.w;
     a->sinks = vis.sinks;
-    a->sink = sink_rows(n_seqs, (long long)B * L, a->w, a->sinks, sink_chunk(cu != nullptr, n_seqs, Hkv, L, a->w));
+    a->chunk = sink_chunk(cu != nullptr, n_seqs, Hkv, L, a->w);
     a->scale = scale;
     a->dtype = dtype;
     return LF_OK;
@@ -147,8 +147,8 @@ size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int 
     size_t n = align256((size_t)(packed ? 1 : n_seqs) * Hq * L * sizeof(float));  // delta
     const Visible vis = clamp_visible(L, w, sinks);
     if (vis.sinks > 0) {
-        const SinkRows r = sink_rows(n_seqs, (packed ? 1LL : n_seqs) * L, vis.w, vis.sinks,
-                                     sink_chunk(packed != 0, n_seqs, Hkv, L, vis.w));
+        const SinkRows r = {n_seqs, packed ? L : n_seqs * L, vis.w, vis.sinks,
+                            sink_chunk(packed != 0, n_seqs, Hkv, L, vis.w)};
         n += align256(sink_part_floats(r, Hkv) * sizeof(float));
     }
     return n;
@@ -228,7 +228,7 @@ size_t lf_paged_attention_workspace_bytes(int n_seqs, int Hq, int Hkv, int T, in
     const int width = max_pages * page_size;
     const PagedPlan p =
         paged_plan(n_seqs, Hq, Hkv, T, imin(max_q_len, T), width, imin(w, width), imin(sinks, width));
-    const size_t rows = p.decode_rows(Hq) + p.tensor_rows(T, Hq);
+    const size_t rows = p.rows(T, Hq);
     return rows * 64 * sizeof(float) + align256(rows * sizeof(float));
 }
 
@@ -279,11 +279,7 @@ lf_status lf_paged_attention_forward(const lf_heads* q, const lf_heads* k_cache,
     a.dtype = dtype;
     a.out = out;
     a.status = d->status;
-    const size_t decode_rows = plan.decode_rows(Hq), rows = decode_rows + plan.tensor_rows(T, Hq);
-    plan.decode_o = static_cast<float*>(workspace);
-    plan.o = plan.decode_o + decode_rows * 64;
-    plan.decode_lse = plan.decode_o + rows * 64;
-    plan.lse = plan.decode_lse + decode_rows;
+    plan.part = static_cast<float*>(workspace);
     return launch_paged_forward(a, plan, (cudaStream_t)stream);
 }
 

@@ -428,18 +428,18 @@ __device__ __forceinline__ bool key_item(const WindowArgs& a, int item, int sink
     p.hk = at / per;
     at -= p.hk * per;
     slot = p.sink ? at % sink_slots : at;
-    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, p.sink ? a.sink.chunk : 128, slot);
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, p.sink ? a.chunk : 128, slot);
     if (t.t0 >= (p.sink ? t.n : t.rows)) return false;
-    p.n_sink = a.sink.any(t.n) ? imin(a.sinks, t.n) : 0;
+    p.n_sink = a.sink().any(t.n) ? imin(a.sinks, t.n) : 0;
     p.b = t.b;
     p.chunk = 0;
     if (p.sink) {
-        p.chunk = t.t0 / a.sink.chunk;
-        if (p.n_sink == 0 || p.chunk < a.sink.first_chunk()) return false;
+        p.chunk = t.t0 / a.chunk;
+        if (p.n_sink == 0 || p.chunk < a.sink().first_chunk()) return false;
         p.c0 = at / sink_slots * 128;
         if (p.c0 >= p.n_sink) return false;  // (more sinks than the sequence has)
         p.q0 = imax(t.t0, p.c0 + a.w + 1);
-        p.q1 = imin(t.t0 + a.sink.chunk, t.n);
+        p.q1 = imin(t.t0 + a.chunk, t.n);
         p.n_keys = p.n_sink;
     } else {
         p.c0 = p.q0 = t.t0;
@@ -640,8 +640,8 @@ dkv_kernel(const __grid_constant__ Maps maps, const __grid_constant__ WindowArgs
                 Target o = {nullptr, nullptr, nullptr};
                 if (key < p->n_sink) {
                     const int start = a.cu ? p->start : p->b * a.L;
-                    const long long row = p->sink ? a.sink.chunk_row(p->b, start, p->chunk) : a.sink.own(p->b, start);
-                    o.part = a.part + ((size_t)p->hk * a.sink.rows + row + key) * 2 * kD + half * 32;
+                    const long long row = p->sink ? a.sink().chunk_row(p->b, start, p->chunk) : a.sink().own(p->b, start);
+                    o.part = a.part + ((size_t)p->hk * a.sink().rows() + row + key) * 2 * kD + half * 32;
                 } else if (!p->sink && key < p->rows) {
                     o.dk = view_row<T>(a.dk, p->batch, p->hk, p->start + key) + half * 32;
                     o.dv = view_row<T>(a.dv, p->batch, p->hk, p->start + key) + half * 32;
@@ -809,7 +809,7 @@ lf_status backward_t(const WindowArgs& a, cudaStream_t stream) {
         !make_heads_map(&mk.dout, dout, a.Hq, a.L, B, G, 64 / G) ||
         !make_heads_map(&mk.k, a.k, a.Hkv, a.L, B, 1, 128) || !make_heads_map(&mk.v, a.v, a.Hkv, a.L, B, 1, 128))
         return LF_ERR_CUDA;
-    const int slots = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.sink.chunk) : 0;
+    const int slots = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.chunk) : 0;
     const long long sink_items = (long long)slots * ((a.sinks + 127) / 128);
     const int per_head = token_slots(a.packed(), a.n_seqs, a.L, 128);
     if (sink_items + per_head > kMostItems / a.Hkv) return LF_ERR_TOO_LARGE;

@@ -284,11 +284,11 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
     float *K = sm, *V = K + kTile, *Q = V + kTile, *dO = Q + kTile, *P = dO + kTile, *S = P + kTile;
     __shared__ float lse_s[kT], delta_s[kT];
     const int G = a.Hq / a.Hkv, TQ = kT / G, hk = blockIdx.y;
-    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.sink.chunk : kT, blockIdx.x % slots);
+    const TokenTile t = token_tile(a.cu, a.lens, a.n_seqs, a.L, kSink ? a.chunk : kT, blockIdx.x % slots);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (kSink ? t.t0 >= t.n : t.t0 >= t.rows) return;
-    const int n_sink = a.sink.any(t.n) ? imin(a.sinks, t.n) : 0;  // keys whose gradients have partials
-    if (kSink && (n_sink == 0 || t.t0 / a.sink.chunk < a.sink.first_chunk())) return;
+    const int n_sink = a.sink().any(t.n) ? imin(a.sinks, t.n) : 0;  // keys whose gradients have partials
+    if (kSink && (n_sink == 0 || t.t0 / a.chunk < a.sink().first_chunk())) return;
     const int c0 = kSink ? (int)(blockIdx.x / slots) * kT : t.t0;
     if (kSink && c0 >= n_sink) return;  // (more sinks than the sequence has)
     const int n_keys = kSink ? n_sink : t.n;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
     int q0, q1;
     if (kSink) {
         q0 = imax(t.t0, a.w + 1);
-        q1 = imin(t.t0 + a.sink.chunk, t.n);
+        q1 = imin(t.t0 + a.chunk, t.n);
     } else {
         q0 = c0;
         q1 = (int)min((long long)t.n, (long long)c0 + kT + a.w);
@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const __grid_constant__ W
     }
     const int seq_start = a.cu ? t.start : t.b * a.L;
     const long long part_row =
-        kSink ? a.sink.chunk_row(t.b, seq_start, t.t0 / a.sink.chunk) : a.sink.own(t.b, seq_start);
+        kSink ? a.sink().chunk_row(t.b, seq_start, t.t0 / a.chunk) : a.sink().own(t.b, seq_start);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int key = c0 + 4 * ty + i;
 #pragma unroll
         for (int c = 0; c < 4; ++c) dk[i][c] *= a.scale;
         if (key < n_sink) {
-            float* p = a.part + ((size_t)hk * a.sink.rows + part_row + key) * 2 * kD + 4 * tx;
+            float* p = a.part + ((size_t)hk * a.sink().rows() + part_row + key) * 2 * kD + 4 * tx;
             store4(p, dk[i]);
             store4(p + kD, dv[i]);
             continue;
@@ -375,16 +375,24 @@ __global__ void __launch_bounds__(128) sink_reduce_kernel(const __grid_constant_
     const int key = blockIdx.x % a.sinks, hk = blockIdx.y, b = blockIdx.x / a.sinks, e = threadIdx.x;
     const int start = a.cu ? iclamp(a.cu[b], 0, a.L) : 0;
     const int n = a.cu ? iclamp(a.cu[b + 1], 0, a.L) - start : (a.lens ? iclamp(a.lens[b], 0, a.L) : a.L);
-    if (key >= n || !a.sink.any(n)) return;
+    if (key >= n || !a.sink().any(n)) return;
     const int seq_start = a.cu ? start : b * a.L;
-    const float* p = a.part + ((size_t)hk * a.sink.rows + key) * 2 * kD + e;
-    auto at = [&](long long row) { return p[(size_t)row * 2 * kD]; };
-    float s = at(a.sink.own(b, seq_start));
-    const int first = a.sink.first_chunk(), end = (n - 1) / a.sink.chunk + 1;
-    s += at(a.sink.chunk_row(b, seq_start, first));
-    const long long next = first + 1 < end ? a.sink.chunk_row(b, seq_start, first + 1) : 0;
-#pragma unroll 16
-    for (int c = 0; c < end - first - 1; ++c) s += at(next + (long long)c * a.sinks);
+    const float* p = a.part + ((size_t)hk * a.sink().rows() + key) * 2 * kD + e;
+    auto at = [&](long long row) -> const float& { return p[(size_t)row * 2 * kD]; };
+    float s = at(a.sink().own(b, seq_start));
+    const int first = a.sink().first_chunk(), end = (n - 1) / a.chunk + 1;
+    s += at(a.sink().chunk_row(b, seq_start, first));
+    // the others, 16 loads at a time in flight
+    const int more = end - first - 1;
+    const float* next = more > 0 ? &at(a.sink().chunk_row(b, seq_start, first + 1)) : nullptr;
+    const size_t step = (size_t)a.sinks * 2 * kD;
+    for (int c = 0; c < more; c += 16) {
+        float x[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) x[u] = c + u < more ? next[(c + u) * step] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) s += x[u];
+    }
     const lf_heads& v = e < kD ? a.dk : a.dv;
     static_cast<T*>(v.data)[(a.cu ? 0 : b) * v.batch_stride + hk * v.head_stride + (start + key) * v.token_stride +
                             (e & (kD - 1))] = from_f<T>(s);
@@ -414,7 +422,7 @@ lf_status launch_window_forward_simt(const WindowArgs& a, cudaStream_t stream) {
 
 lf_status launch_window_backward_simt(const WindowArgs& a, cudaStream_t stream) {
     const int TQ = kT / a.heads_group(), tiles = token_slots(a.packed(), a.n_seqs, a.L, kT);
-    const int chunks = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.sink.chunk) : 0;
+    const int chunks = a.sinks > 0 ? token_slots(a.packed(), a.n_seqs, a.L, a.chunk) : 0;
     const long long sink_tiles = (long long)chunks * ((a.sinks + kT - 1) / kT);
     if (sink_tiles > INT32_MAX) return LF_ERR_TOO_LARGE;
     lf_status st = launch(dq_kernel, dim3(token_slots(a.packed(), a.n_seqs, a.L, TQ), a.Hkv), 5, stream, a);

@@ -583,7 +583,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     }
                     if (row_stored) {
                         if (kPaged && p->part) {
-                            float4* d = reinterpret_cast<float4*>(pp.o + ((size_t)p->z * ((size_t)L * a.Hq) + orow) * kD + h * 32);
+                            float4* d = reinterpret_cast<float4*>(pp.o(a.Hq) + ((size_t)p->z * ((size_t)L * a.Hq) + orow) * kD + h * 32);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         } else {
@@ -593,7 +593,7 @@ window_kernel(const __grid_constant__ Maps maps, const __grid_constant__ A a, co
                     __syncwarp();
                 }
                 if (row_stored) {
-                    if (kPaged && p->part) pp.lse[(size_t)p->z * ((size_t)L * a.Hq) + orow] = lse2;
+                    if (kPaged && p->part) pp.lse(L, a.Hq)[(size_t)p->z * ((size_t)L * a.Hq) + orow] = lse2;
                     if constexpr (!kPaged)
                         a.lse[((size_t)p->batch * a.Hq + p->hk * G + r_head) * L + p->start + tok] = lse2 * kLn2;
                 }

@@ -32,12 +32,12 @@ void slot(int n, int Hq, int Hkv, int T, int mq, int width, int w, int s, int b,
     PagedPlan p = paged_plan(n, Hq, Hkv, T, mq, width, w, s);
     o[0] = p.decode_slot(b, start, t); o[1] = p.decode_tokens;
 }
-void sink_layout(int n, long long T, int w, int s, int chunk, long long* o) {
-    SinkRows r = sink_rows(n, T, w, s, chunk);
-    o[0] = r.rows; o[1] = r.how; o[2] = r.first_chunk();
+void sink_layout(int n, int T, int w, int s, int chunk, long long* o) {
+    SinkRows r = {n, T, w, s, chunk};
+    o[0] = r.rows(); o[1] = r.one() == r.by_seq() ? 0 : r.one() == r.by_start() ? 1 : 2; o[2] = r.first_chunk();
 }
-long long sink_row(int n, long long T, int w, int s, int chunk, int b, int start, int len, int k) {
-    SinkRows r = sink_rows(n, T, w, s, chunk);
+long long sink_row(int n, int T, int w, int s, int chunk, int b, int start, int len, int k) {
+    SinkRows r = {n, T, w, s, chunk};
     return !r.any(len) ? -1 : k < 0 ? r.own(b, start) : r.chunk_row(b, start, k);
 }
 }
@@ -206,7 +206,7 @@ def _sink_rows(P, lens, starts, T, w, s, chunk):
     P.sink_row.restype = ll
     o = (ll * 3)()
     n = len(lens)
-    P.sink_layout(n, ll(T), w, s, chunk, o)
+    P.sink_layout(n, T, w, s, chunk, o)
     rows, how, first = o
     seen = set()
     for b, m in enumerate(lens):
@@ -214,12 +214,12 @@ def _sink_rows(P, lens, starts, T, w, s, chunk):
         want = sorted({i // chunk for i in range(w + 1, m)})
         assert not want or want[0] == first
         for k in [-1] + want if want else []:
-            r = P.sink_row(n, ll(T), w, s, chunk, b, starts[b], m, k)
+            r = P.sink_row(n, T, w, s, chunk, b, starts[b], m, k)
             for key in range(min(s, m)):
                 assert 0 <= r + key < rows and (r + key) not in seen, (b, m, k, key)
                 seen.add(r + key)
         if not want:
-            assert P.sink_row(n, ll(T), w, s, chunk, b, starts[b], m, 0) == -1
+            assert P.sink_row(n, T, w, s, chunk, b, starts[b], m, 0) == -1
     return rows, how
 
 
