@@ -427,9 +427,11 @@ lf_status lf_selftest_bounded_wait(unsigned long long limit_ns, lf_stream_t stre
  * of size 1 is not used.  So [B, H, L, 64], [T, H, 64] and slices of a fused
  * projection's output all fit.
  *
- * The calls from here on keep no state of their own between calls.  The
- * first call of the library on a device allocates its status word: make it
- * before any stream capture; every call after that may be captured.
+ * The calls from here on keep no state of their own between calls.  No output
+ * or workspace may overlap an input or another output.  The first call of the
+ * library on a device allocates its status word: make it before any stream
+ * capture; every call after that may be captured.  (lf_version() does not tell
+ * a library with these calls from one without: look for the symbol.)
  */
 typedef struct {
     void* data;
@@ -469,7 +471,10 @@ lf_status lf_window_attention_forward(const lf_heads* q, const lf_heads* k, cons
                                       int Hkv, int L, int w, int sinks, float scale, lf_dtype dtype,
                                       lf_stream_t stream, void* out, float* lse);
 
-/* Bytes of workspace lf_window_attention_backward needs (0 on bad sizes). */
+/* Bytes of workspace lf_window_attention_backward needs (0 on bad sizes): 4
+ * for each row of lse, and where sinks lie outside windows up to 512 * Hkv for
+ * each of sinks * (2 * sequences of more than w + 1 tokens + chunks of at
+ * least 64 tokens). */
 size_t lf_window_attention_backward_workspace_bytes(int packed, int n_seqs, int Hq, int Hkv, int L, int w, int sinks);
 
 /*

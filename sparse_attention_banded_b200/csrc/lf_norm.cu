@@ -19,6 +19,12 @@
 // TB/s of a copy (168 MB; the second kernel's sums, 5 us, and two rows in
 // flight per group in the backward, which registers bound, keep it there);
 // 5001 x 1537 fp32, an odd width by single elements, 37 us, 4.1 TB/s.
+// Where a thread's part of a row does not fit its registers it spills (bytes
+// a thread, TB/s of the pass): forward of 4097 to 8192 columns, 64 registers
+// for two blocks of 512 threads per SM, 260 and 612, 1.9 at 8192 x 5120 bf16
+// against 3.9 at 8192 x 4096; above 8192 columns backward, 470 to 1040, 1.5
+// at 2048 x 16384 bf16; backward of 16-bit rows by single elements, 344 to
+// 480 at any width, 0.8 at 8192 x 2050 bf16 against 3.2 with 16-byte loads.
 #include "lf_convert.cuh"
 #include "lf_tc_tiles.cuh"
 #include "lf_window.h"

@@ -73,6 +73,9 @@ inline long long most_blocks(int max_q, int width, int w, int sinks, int bk) {
 // CTAs per SM; more run four per SM.  Both ways, 8 heads, window 2048: 128
 // items 29 and 39 us, 256 39 and 47, 320 41 and 54, 448 68 and 64, 2048 237
 // and 210; window 128: 256 12.4 and 14.4, 320 18.0 and 17.2, 2048 57 and 51.
+// One count for all windows: with long ones the crossing lies higher, and
+// between 296 and some 400 items the other way would be up to a quarter
+// faster.
 constexpr int kAheadItems = 2 * 148;
 
 // w and sinks clamped to the table's width.
@@ -99,11 +102,21 @@ inline PagedPlan paged_plan(int n_seqs, int Hq, int Hkv, int T, int max_q, int w
     }
     if (p.tensor) {
         // In units of 0.1 us: up to 296 items run at once (two per SM, worked
-        // on ahead), a block in 8; of more, 592 run at a time (four per SM),
-        // a block in 22.  Pieces are joined by a further kernel, worth 80 (10
-        // when it runs anyway, for the decode kernel).  Next to single
-        // tokens, which are no tiles, a quarter of the sequences are taken to
-        // end in one.
+        // on ahead), a block in 8 (128 items of 34 blocks: 29 us); of more,
+        // 592 run at a time (four per SM), a block in 22 (measured 17, 2048
+        // items of 18 blocks 135 us and of 66 471; 22 keeps to one wave more
+        // readily: of calls that differ, 48 us against 52 with 16, 92 and
+        // 101, 165 and 178, 82 and 75).  Pieces are joined by a further
+        // kernel, worth 80 (8 us for 32768 rows of two pieces; 10 when it
+        // runs anyway, for the decode kernel).
+        // The device alone knows which sequences are single tokens, no tiles
+        // of their own: a quarter are taken to end in a tile.  With none, a
+        // quarter and all of them (us; 16 / 4 heads, contexts to 8000): 16
+        // mixed lengths window 1024 29, 28, 32; 512 tokens and 64 single ones
+        // window 1024 43, 45, 53, no window 110, 124, 126; 32 chunks of 33
+        // and 32 single ones 47, 43, 53 and 199, 165, 174.  Pieces against
+        // none, one chunk alone: 1024 tokens of 16384 144 and 209, 128 of
+        // 30000 48 and 373.
         const int join = p.decode && p.decode_splits > 1 ? 10 : 80;
         const long long blocks = most_blocks(max_q, width, w, sinks, 64);
         const long long tiles = ((long long)T / (128 / G) + (p.decode ? (n_seqs + 3) / 4 : n_seqs)) * Hkv;

@@ -98,6 +98,12 @@ struct Layout {
     static constexpr int kBufs = kAhead ? 2 : 1;  // of S
     // Registers a thread at launch; a block's share is split anew.  (Four
     // CTAs, the padded batch: 24 and 104 59 us, 32 and 96 60, 40 and 88 66.)
+    // Code of warps 4 to 7 must stay inline: after they have given registers
+    // away, a call out of line (a device printf, a 64-bit division, a helper
+    // that is not inlined) may use more than the warp has left, which is an
+    // illegal instruction.  ptxas keeps what is inlined to the share; four
+    // CTAs of the paged form spill 224 and 368 bytes for it, the other 80 and
+    // 92.
     static constexpr uint32_t kRegsLaunch = kAhead ? 128 : 64, kRegsProducer = kAhead ? 96 : 24,
                               kRegsSoftmax = kAhead ? 160 : 104;
     static_assert(4 * 32 * kRegsProducer + 4 * 32 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");

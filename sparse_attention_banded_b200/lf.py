@@ -538,7 +538,8 @@ def lf_window_attention_forward(q, k, v, w: int, sinks: int = 0, scale: float = 
     strides, last dimension contiguous), with seq_lens [B] int32 tokens per
     row when padded; or packed q [T, Hq, 64], k, v [T, Hkv, 64] with
     cu_seqlens [n + 1] int32.  Returns (out [B, L, Hq*64] or [T, Hq*64], lse
-    [B, Hq, L] or [1, Hq, T] float32, for the backward pass)."""
+    [B, Hq, L] or [1, Hq, T] float32, for the backward pass).  Not an autograd
+    function: :func:`lf_window_attention_backward` computes the gradients."""
     w, sinks = _int32(w=w, sinks=sinks)
     n, Hq, Hkv, L, o_shape, l_shape = _window_shape(q, k, v, cu_seqlens, seq_lens)
     with _on(q, stream, k, v, cu_seqlens, seq_lens, out, lse):
@@ -677,7 +678,8 @@ def _rows(name, t):
 def lf_layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
     """Layer norm of the rows of x [..., N]; gamma, beta [N] float32 or None.
     Returns (y, mean, rstd), mean and rstd [rows] float32 for the backward
-    pass."""
+    pass.  Not an autograd function: :func:`lf_layer_norm_backward` computes
+    the gradients."""
     px, rows, N, stride = _rows("x", x)
     with _on(x, stream, gamma, beta, out, mean, rstd):
         if gamma is not None:
