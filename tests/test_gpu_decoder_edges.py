@@ -259,3 +259,44 @@ def test_dv_of_late_keys_in_a_long_context(dtype, n):
     want = (p * do[0, -64:].double()).flip(0).cumsum(0).flip(0)
     u, z = half_step(DT[dtype]), subnormal_half_step(DT[dtype])
     check("dv", dv[0, 0, -64:], want, (2 * u + 2.0 ** -17) * want + z)  # (all terms are positive)
+
+
+@pytest.mark.parametrize("rows", [(1 << 31) - 1, (1 << 31) - 8])
+def test_layer_norm_of_the_last_row_counts(rows):
+    """One column: x is its own mean, y is beta, dx is 0."""
+    x = torch.empty(rows, 1, dtype=torch.float16, device="cuda")
+    x.view(-1)[:] = 1.0
+    x[-5:, 0] = torch.arange(5, dtype=torch.float16, device="cuda")
+    gamma, beta = torch.full((1,), 2.0, device="cuda"), torch.full((1,), 0.5, device="cuda")
+    y, mean, rstd = lf.lf_layer_norm_forward(x, gamma, beta)
+    for at in (slice(0, 10), slice(rows // 2, rows // 2 + 10), slice(rows - 10, rows)):
+        assert torch.equal(mean[at], x[at, 0].float()) and bool((y[at] == 0.5).all())
+    y.fill_(7.0)
+    dx, dgamma, _ = lf.lf_layer_norm_backward(x, x, gamma, mean, rstd, dx=y)
+    for at in (slice(0, 10), slice(rows // 2, rows // 2 + 10), slice(rows - 10, rows)):
+        assert bool((dx[at] == 0).all())
+    assert float(dgamma) == 0
+    del x, y, mean, rstd, dx
+    torch.cuda.empty_cache()  # 35 GB
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_layer_norm_past_2_31_elements(dtype):
+    rows, N = (1 << 21) + 5, 1030
+    x = torch.empty(rows, N, dtype=DT[dtype], device="cuda")
+    g = torch.Generator().manual_seed(9)
+    few = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device="cuda")
+    x.fill_(1.0)
+    x[:, ::2] = -1.0
+    x[few] = torch.randn(5, N, generator=g).to(DT[dtype]).cuda()
+    dy = x.clone()
+    y, mean, rstd = lf.lf_layer_norm_forward(x)
+    dx, _, dbeta = lf.lf_layer_norm_backward(dy, x, None, mean, rstd)
+    small = x[few].clone()
+    y2, mean2, rstd2 = lf.lf_layer_norm_forward(small)
+    dx2, _, dbeta2 = lf.lf_layer_norm_backward(small, small, None, mean2, rstd2)
+    assert torch.equal(y[few], y2) and torch.equal(mean[few], mean2) and torch.equal(dx[few], dx2)
+    # the other rows are +-1 in turn: integers below 2^24 a block, exact; the
+    # five others' sums are rounded on the way (2^-24 of 2^21, a few times)
+    want = dbeta2.double() + torch.where(torch.arange(N, device="cuda") % 2 == 0, -1.0, 1.0).double() * (rows - 5)
+    assert float((dbeta.double() - want).abs().max()) <= 8 * 2.0 ** -3
